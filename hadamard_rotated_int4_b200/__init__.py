@@ -18,6 +18,10 @@ Names follow include/hbl.h:
   bitlinear_forward(X, W_packed, alpha, act_bits, flags)            -> Y bf16 [M, N]
   rotate_weights(W, signs)                -> W_rot fp32 [N, K]
   kv_quant(X, bits)                       -> (codes uint8 [rows, D*bits/8], scales fp32 [rows])
+  kv_cache_alloc(pages, page_size, heads, D, bits, device)          -> KvCache (paged, low-bit)
+  kv_cache_write(cache, K, V, cu_seqlens, kv_lens, block_table)     (quantises new rows into pages)
+  kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows)      -> (K, V) [rows, heads, D]
+  kv_attention(Q, cache, cu_seqlens, kv_lens, block_table)          -> O bf16 [rows, q heads, D] (, lse)
 """
 import ctypes
 import os
@@ -41,10 +45,32 @@ EXPORTS = ("hbl_status_string", "hbl_version", "hbl_workspace_size", "hbl_worksp
            "hbl_hbitlinear_forward_hostio",
            "hbl_ternary_gemv_noalloc", "hbl_norm_transform", "hbl_norm_quant",
            "hbl_bitlinear_forward", "hbl_rotate_weights", "hbl_kv_quant",
+           "hbl_kv_cache_write", "hbl_kv_cache_read", "hbl_kv_attention_workspace",
+           "hbl_kv_attention",
            "hbl_expand_ternary", "hbl_ternary_gemm_s8w", "hbl_selftest_bounded_wait",
            "hbl_probe_tc_int8")
 
 _lib = None
+
+
+class _CacheArgs(ctypes.Structure):  # hbl_kv_cache
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+               [(n, ctypes.c_int) for n in ("num_pages", "page_size", "num_kv_heads", "head_dim",
+                                            "bits")]
+
+
+class _BatchArgs(ctypes.Structure):  # hbl_kv_batch
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_seqlens", "kv_lens", "block_table")] + \
+               [(n, ctypes.c_int) for n in ("num_seqs", "pages_per_seq", "rows")]
+
+
+class _AttnArgs(ctypes.Structure):  # hbl_kv_attn
+    _fields_ = [("Q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("O", ctypes.c_void_p),
+                ("o_row_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("num_heads", ctypes.c_int), ("max_rows", ctypes.c_int),
+                ("max_kv", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int),
+                ("window", ctypes.c_int)]
 
 
 class HblError(RuntimeError):
@@ -100,6 +126,15 @@ def lib():
         L.hbl_rotate_weights.argtypes = [P, P, I, I, P, P, P]
         L.hbl_kv_quant.restype = I
         L.hbl_kv_quant.argtypes = [P, I64, I, I, F, P, P, P, P]
+        CA, BA, AA = (ctypes.POINTER(t) for t in (_CacheArgs, _BatchArgs, _AttnArgs))
+        L.hbl_kv_cache_write.restype = I
+        L.hbl_kv_cache_write.argtypes = [CA, BA, P, I64, I64, P, I64, I64, F, P, P]
+        L.hbl_kv_cache_read.restype = I
+        L.hbl_kv_cache_read.argtypes = [CA, BA, P, P, I, P, P]
+        L.hbl_kv_attention_workspace.restype = I
+        L.hbl_kv_attention_workspace.argtypes = [CA, BA, AA, ctypes.POINTER(SZ)]
+        L.hbl_kv_attention.restype = I
+        L.hbl_kv_attention.argtypes = [CA, BA, AA, P, SZ, P, P]
         L.hbl_expand_ternary.restype = I
         L.hbl_expand_ternary.argtypes = [P, I, I, P, P, P]
         L.hbl_ternary_gemm_s8w.restype = I
@@ -368,6 +403,210 @@ def kv_quant(X, bits, eps=1e-5, out=None, status=None):
     _check(lib().hbl_kv_quant(_ptr(X), rows, D, int(bits), float(eps), _ptr(codes),
                               _ptr(scales), _ptr(status), _stream()), "hbl_kv_quant")
     return codes, scales[:rows]
+
+
+# ------------------------------------------------------- paged low-bit KV cache
+
+class KvCache:
+    """A paged low-bit K/V cache: uint8 codes [pages, heads, page_size, D*bits/8]
+    and fp32 scales [pages, heads, page_size], for K and for V (hbl_kv_cache)."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "num_pages", "num_kv_heads",
+                 "page_size", "head_dim", "bits", "device", "_args")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim):
+        import torch
+
+        for t, dt, name in ((k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
+                            (k_scales, torch.float32, "k_scales"),
+                            (v_scales, torch.float32, "v_scales")):
+            _dev(t, dt, name)
+        shape = k_scales.shape
+        if len(shape) != 3 or k_codes.dim() != 4 or k_codes.shape[:3] != shape or \
+                v_codes.shape != k_codes.shape or v_scales.shape != shape:
+            raise ValueError("codes must be [pages, heads, page_size, D*bits/8] and scales "
+                             "[pages, heads, page_size], alike for K and V")
+        if not k_codes.device == v_codes.device == k_scales.device == v_scales.device:
+            raise ValueError("the cache's tensors must be on one device")
+        self.num_pages, self.num_kv_heads, self.page_size = shape
+        self.head_dim, self.device = int(head_dim), k_codes.device
+        self.bits = k_codes.shape[3] * 8 // self.head_dim if self.head_dim > 0 else 0
+        if self.head_dim < 1 or kv_code_bytes(self.head_dim, self.bits) != k_codes.shape[3]:
+            raise ValueError("the codes' last dimension must be head_dim * bits / 8 bytes")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
+                                                                   v_scales)
+        self._args = _CacheArgs(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                v_scales.data_ptr(), self.num_pages, self.page_size,
+                                self.num_kv_heads, self.head_dim, self.bits)
+
+
+def kv_cache_alloc(num_pages, page_size, num_kv_heads, head_dim, bits, device):
+    """An empty KvCache (its pages need no initial values)."""
+    import torch
+
+    shape = (num_pages, num_kv_heads, page_size)
+    codes = [torch.empty(shape + (kv_code_bytes(head_dim, bits),), dtype=torch.uint8,
+                         device=device) for _ in range(2)]
+    scales = [torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2)]
+    return KvCache(codes[0], scales[0], codes[1], scales[1], head_dim)
+
+
+def _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows):
+    """hbl_kv_batch of int32 CUDA tensors on the cache's device."""
+    import torch
+
+    for t, name, dims in ((cu_seqlens, "cu_seqlens", 1), (kv_lens, "kv_lens", 1),
+                          (block_table, "block_table", 2)):
+        _dev(t, torch.int32, name)
+        if t.dim() != dims:
+            raise ValueError("%s must have %d dimension(s)" % (name, dims))
+        if t.device != cache.device:
+            raise ValueError("%s must be on the cache's device" % name)
+    n = kv_lens.shape[0]
+    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+        raise ValueError("cu_seqlens must have one entry more, block_table as many rows as "
+                         "kv_lens has entries")
+    return _BatchArgs(cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n,
+                      block_table.shape[1], int(rows))
+
+
+def _kv_rows(t, cache, name, heads=None):
+    """Checks a strided bf16 [rows, heads, D] tensor; returns its strides."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.device != cache.device:
+        raise ValueError("%s must be on the cache's device" % name)
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s must be [rows, heads, head_dim] like the cache" % name)
+    sr, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    # the stride of a dimension of one is never used
+    return sr if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0
+
+
+def _on(device):
+    """The device's current stream, and the device made current for the call."""
+    import torch
+
+    index = device.index
+    guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return guard, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _kv_call(what, device, *args):
+    guard, stream = _on(device)
+    if guard is None:
+        status = getattr(lib(), what)(*args, stream)
+    else:
+        with guard:
+            status = getattr(lib(), what)(*args, stream)
+    _check(status, what)
+
+
+def _kv_status(status, cache):
+    import torch
+
+    if status is not None:
+        _dev(status, torch.int32, "status")
+        if status.device != cache.device:
+            raise ValueError("status must be on the cache's device")
+    return _ptr(status)
+
+
+def kv_cache_write(cache, K, V, cu_seqlens, kv_lens, block_table, eps=1e-5, status=None):
+    """hbl_kv_cache_write: quantise the packed new rows K, V [rows, heads, D] (any
+    row and head strides that are multiples of 8) into the batch's pages."""
+    ks = _kv_rows(K, cache, "K", cache.num_kv_heads)
+    vs = _kv_rows(V, cache, "V", cache.num_kv_heads)
+    if K.shape != V.shape:
+        raise ValueError("K and V must have the same shape")
+    batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, K.shape[0])
+    _kv_call("hbl_kv_cache_write", cache.device, cache._args, batch, K.data_ptr(), ks[0], ks[1],
+             V.data_ptr(), vs[0], vs[1], float(eps), _kv_status(status, cache))
+
+
+def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out=None,
+                  status=None):
+    """hbl_kv_cache_read: the last cu_seqlens[b+1] - cu_seqlens[b] positions of each
+    sequence as (K, V) [rows, heads, D], bf16 (default) or torch.float32."""
+    import torch
+
+    shape = (int(rows), cache.num_kv_heads, cache.head_dim)
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32, got %s" % dtype)
+        K = torch.empty(shape, dtype=dtype, device=cache.device)
+        V = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        K, V = out
+        dtype = K.dtype if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out must be torch.bfloat16 or torch.float32, got %s" % dtype)
+        for t in (K, V):
+            _dev(t, dtype, "out")
+            if tuple(t.shape) != shape or t.device != cache.device:
+                raise ValueError("out must be two [rows, heads, D] tensors on the cache's device")
+    batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
+    _kv_call("hbl_kv_cache_read", cache.device, cache._args, batch, K.data_ptr(), V.data_ptr(),
+             1 if dtype == torch.float32 else 0, _kv_status(status, cache))
+    return K, V
+
+
+def kv_attention_workspace_size(rows, num_heads, cache, num_seqs, pages_per_seq, max_rows=0,
+                                max_kv=0, causal=True, window=0):
+    """Workspace bytes of kv_attention for these sizes."""
+    batch = _BatchArgs(None, None, None, int(num_seqs), int(pages_per_seq), int(rows))
+    args = _AttnArgs(None, 0, 0, None, 0, 0, None, int(num_heads), int(max_rows or 0),
+                     int(max_kv or 0), 1.0, int(bool(causal)), int(window))
+    need = ctypes.c_size_t(0)
+    _check(lib().hbl_kv_attention_workspace(cache._args, batch, args, ctypes.byref(need)),
+           "hbl_kv_attention_workspace")
+    return need.value
+
+
+def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_kv=None,
+                 scale=None, causal=True, window=0, want_lse=False, ws=None, out=None,
+                 status=None):
+    """hbl_kv_attention: the packed rows Q [rows, q heads, D] attend to everything
+    their sequences have cached, their own positions among it.  scale defaults to
+    1/sqrt(D); window 0 is none.  max_rows (no sequence has more rows) and max_kv
+    (about the longest sequence) are host-side sizes that the launch is planned
+    with; without them the row count and the block table's width are taken.
+    Returns O (out if given), with want_lse also lse fp32 [rows, q heads]."""
+    import torch
+
+    qs = _kv_rows(Q, cache, "Q")
+    rows, heads, D = Q.shape
+    O = torch.empty((rows, heads, D), dtype=torch.bfloat16, device=cache.device) \
+        if out is None else out
+    os_ = _kv_rows(O, cache, "out", heads)
+    if O.shape[0] != rows:
+        raise ValueError("out must have Q's shape")
+    lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) \
+        if want_lse else None
+    batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
+    args = _AttnArgs(Q.data_ptr(), qs[0], qs[1], O.data_ptr(), os_[0], os_[1],
+                     None if lse is None else lse.data_ptr(), heads, int(max_rows or 0),
+                     int(max_kv or 0), D ** -0.5 if scale is None else float(scale),
+                     int(bool(causal)), int(window))
+    if ws is None:
+        need = ctypes.c_size_t(0)
+        _check(lib().hbl_kv_attention_workspace(cache._args, batch, args, ctypes.byref(need)),
+               "hbl_kv_attention_workspace")
+        if need.value:
+            ws = _workspace(need.value, cache.device)
+    elif not ws.is_cuda or ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the cache's device")
+    _kv_call("hbl_kv_attention", cache.device, cache._args, batch, args, _ptr(ws),
+             0 if ws is None else ws.numel() * ws.element_size(), _kv_status(status, cache))
+    return (O, lse) if want_lse else O
 
 
 # ------------------------------------------------------- expanded weights

@@ -718,6 +718,148 @@ hbl_status hbl_kv_quant(const uint16_t* X, int64_t rows, int D, int bits, float 
                            static_cast<cudaStream_t>(stream), sms);
 }
 
+// The cache's and the batch's scalars; their pointers only matter when there is work.
+static hbl_status check_kv_shape(const hbl_kv_cache* c, const hbl_kv_batch* b) {
+    if (!c || !b) return HBL_ERR_INVALID_ARG;
+    if (c->bits != 2 && c->bits != 3 && c->bits != 4 && c->bits != 8) return HBL_ERR_INVALID_ARG;
+    const int D = c->head_dim;
+    if (D != 32 && D != 64 && D != 128 && D != 256) return HBL_ERR_SHAPE;
+    if (c->num_pages < 1 || c->num_kv_heads < 1 || c->num_kv_heads > 65535) return HBL_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > 65536) return HBL_ERR_SHAPE;
+    if (b->num_seqs < 0 || b->pages_per_seq < 0 || b->rows < 0) return HBL_ERR_SHAPE;
+    // positions are 32-bit
+    if ((int64_t)b->pages_per_seq * c->page_size > 0x7fffffffll) return HBL_ERR_SHAPE;
+    return HBL_OK;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static hbl_status check_kv_pointers(const hbl_kv_cache* c, const hbl_kv_batch* b) {
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return HBL_ERR_INVALID_ARG;
+    if (!b->cu_seqlens || !b->kv_lens || (!b->block_table && b->pages_per_seq > 0))
+        return HBL_ERR_INVALID_ARG;
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
+        !aligned16(c->v_scales) || !aligned4(b->cu_seqlens) || !aligned4(b->kv_lens) ||
+        !aligned4(b->block_table))
+        return HBL_ERR_ALIGNMENT;
+    return HBL_OK;
+}
+static KvCache kv_cache_of(const hbl_kv_cache* c) {
+    return {c->k_codes,   c->k_scales,  c->v_codes,      c->v_scales, c->num_pages,
+            c->page_size, c->num_kv_heads, c->head_dim, c->bits};
+}
+static KvBatch kv_batch_of(const hbl_kv_batch* b) {
+    return {b->cu_seqlens, b->kv_lens, b->block_table, b->num_seqs, b->pages_per_seq, b->rows};
+}
+// 16-byte vectors of a strided tensor start on 16-byte boundaries.
+static bool strides8(int64_t row, int64_t head) { return row % 8 == 0 && head % 8 == 0; }
+
+hbl_status hbl_kv_cache_write(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                              const uint16_t* K, int64_t k_row_stride, int64_t k_head_stride,
+                              const uint16_t* V, int64_t v_row_stride, int64_t v_head_stride,
+                              float eps, int32_t* dev_status, void* stream) {
+    hbl_status st = check_kv_shape(cache, batch);
+    if (st != HBL_OK) return st;
+    if (!finite_nonneg(eps)) return HBL_ERR_INVALID_ARG;
+    if (batch->rows == 0 || batch->num_seqs == 0) return HBL_OK;
+    st = check_kv_pointers(cache, batch);
+    if (st != HBL_OK) return st;
+    if (!K || !V) return HBL_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V) || !strides8(k_row_stride, k_head_stride) ||
+        !strides8(v_row_stride, v_head_stride))
+        return HBL_ERR_ALIGNMENT;
+    int sms = 0;
+    st = device(&sms);
+    if (st != HBL_OK) return st;
+    const KvStates x = {K, V, k_row_stride, k_head_stride, v_row_stride, v_head_stride};
+    return launch_kv_cache_write(kv_cache_of(cache), kv_batch_of(batch), x, eps, dev_status,
+                                 static_cast<cudaStream_t>(stream), sms);
+}
+
+hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_batch* batch, void* K_out,
+                             void* V_out, int out_fp32, int32_t* dev_status, void* stream) {
+    hbl_status st = check_kv_shape(cache, batch);
+    if (st != HBL_OK) return st;
+    if (out_fp32 != 0 && out_fp32 != 1) return HBL_ERR_INVALID_ARG;
+    if (batch->rows == 0 || batch->num_seqs == 0) return HBL_OK;
+    st = check_kv_pointers(cache, batch);
+    if (st != HBL_OK) return st;
+    if (!K_out || !V_out) return HBL_ERR_INVALID_ARG;
+    if (!aligned16(K_out) || !aligned16(V_out)) return HBL_ERR_ALIGNMENT;
+    int sms = 0;
+    st = device(&sms);
+    if (st != HBL_OK) return st;
+    return launch_kv_cache_read(kv_cache_of(cache), kv_batch_of(batch), K_out, V_out,
+                                out_fp32 != 0, dev_status, static_cast<cudaStream_t>(stream), sms);
+}
+
+static hbl_status check_kv_attn(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                                const hbl_kv_attn* a) {
+    hbl_status st = check_kv_shape(cache, batch);
+    if (st != HBL_OK) return st;
+    if (!a) return HBL_ERR_INVALID_ARG;
+    if (!isfinite(a->scale) || a->window < 0 || (a->causal != 0 && a->causal != 1))
+        return HBL_ERR_INVALID_ARG;
+    if (a->num_heads < 1 || a->num_heads % cache->num_kv_heads != 0 || a->num_heads > 65535 ||
+        a->max_rows < 0 || a->max_kv < 0)
+        return HBL_ERR_SHAPE;
+    return HBL_OK;
+}
+static KvAttn kv_attn_of(const hbl_kv_cache* c, const hbl_kv_batch* b, const hbl_kv_attn* a) {
+    KvAttn k = {};
+    k.q = a->Q;
+    k.o = a->O;
+    k.lse = a->lse;
+    k.q_row = a->q_row_stride;
+    k.q_head = a->q_head_stride;
+    k.o_row = a->o_row_stride;
+    k.o_head = a->o_head_stride;
+    k.heads = a->num_heads;
+    k.group = a->num_heads / c->num_kv_heads;
+    const int64_t cap = (int64_t)b->pages_per_seq * c->page_size;
+    k.max_rows = a->max_rows == 0 || a->max_rows > b->rows ? b->rows : a->max_rows;
+    k.max_kv = a->max_kv == 0 || a->max_kv > cap ? (int)cap : a->max_kv;
+    k.scale = a->scale;
+    k.causal = a->causal;
+    k.window = a->window;
+    return k;
+}
+
+hbl_status hbl_kv_attention_workspace(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                                      const hbl_kv_attn* attn, size_t* bytes) {
+    if (bytes == nullptr) return HBL_ERR_INVALID_ARG;
+    *bytes = 0;
+    const hbl_status st = check_kv_attn(cache, batch, attn);
+    if (st != HBL_OK) return st;
+    if (batch->rows == 0 || batch->num_seqs == 0) return HBL_OK;
+    *bytes = kv_attention_workspace(kv_cache_of(cache), kv_batch_of(batch),
+                                    kv_attn_of(cache, batch, attn));
+    return HBL_OK;
+}
+
+hbl_status hbl_kv_attention(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                            const hbl_kv_attn* attn, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, void* stream) {
+    hbl_status st = check_kv_attn(cache, batch, attn);
+    if (st != HBL_OK) return st;
+    if (batch->rows == 0 || batch->num_seqs == 0) return HBL_OK;
+    st = check_kv_pointers(cache, batch);
+    if (st != HBL_OK) return st;
+    if (!attn->Q || !attn->O) return HBL_ERR_INVALID_ARG;
+    if (!aligned16(attn->Q) || !aligned16(attn->O) || !aligned4(attn->lse) ||
+        !strides8(attn->q_row_stride, attn->q_head_stride) ||
+        !strides8(attn->o_row_stride, attn->o_head_stride))
+        return HBL_ERR_ALIGNMENT;
+    const KvCache c = kv_cache_of(cache);
+    const KvBatch b = kv_batch_of(batch);
+    const KvAttn a = kv_attn_of(cache, batch, attn);
+    const size_t need = kv_attention_workspace(c, b, a);
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return HBL_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(ws)) return HBL_ERR_ALIGNMENT;
+    int sms = 0;
+    st = device(&sms);
+    if (st != HBL_OK) return st;
+    return launch_kv_attention(c, b, a, ws, dev_status, static_cast<cudaStream_t>(stream), sms);
+}
+
 hbl_status hbl_expand_ternary(const uint32_t* W_packed, int N, int K, int8_t* W_s8,
                               int32_t* dev_status, void* stream) {
     (void)dev_status;

@@ -1,0 +1,178 @@
+// hbl_kv.cuh -- device helpers shared by the KV kernels: the absmax quantiser of
+// one head row, the packed-code layout, and the paged batch's addressing.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "hbl_internal.cuh"
+#include "hbl_launch.h"
+
+namespace hbl {
+
+// ------------------------------------------------------------ codes of 16 values
+// A lane holds 16 values of a row, D/16 lanes a row.  Its 16 codes are 16*B
+// contiguous bits: two halves of 8 codes, code i of a half at bits [B*i, B*i+B).
+constexpr int kKvVpl = 16;
+
+template <int B>
+using KvHalf = typename std::conditional<(8 * B <= 32), uint32_t, uint64_t>::type;
+
+// Quantises a row spread over D/16 neighbouring lanes (bf16 bits in raw):
+// gamma = max|x| over those lanes, inv = Qp / (gamma + eps) (one division),
+// u = rhe(x * inv) + 2^(B-1), each product rounded once by an fma with
+// 1.5 * 2^23.  No clamp is needed: |x| <= gamma, so |x * inv| <= Qp up to the
+// rounding of inv (well under half a unit).  Returns gamma / Qp.
+// Every lane of the warp calls it (the max goes through shuffles).
+template <int D, int B>
+__device__ __forceinline__ float kv_quant16(const uint4 (&raw)[2], float eps, KvHalf<B> (&h)[2]) {
+    constexpr int QP = (1 << (B - 1)) - 1;
+    constexpr int32_t kMagicBits = 0x4B400000;  // 1.5 * 2^23
+    const float qp = (float)QP;
+    float x[kKvVpl];
+    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                           raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = bf16x2_to_f2(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+    float g = 0.f;
+#pragma unroll
+    for (int i = 0; i < kKvVpl; ++i) g = fmaxf(g, fabsf(x[i]));
+#pragma unroll
+    for (int o = 1; o < D / kKvVpl; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    const float den = __fadd_rn(g, eps);
+    const float inv = den > 0.f ? __fdiv_rn(qp, den) : 0.f;
+    h[0] = 0;
+    h[1] = 0;
+#pragma unroll
+    for (int i = 0; i < kKvVpl; ++i) {
+        const int32_t b = __float_as_int(__fmaf_rn(x[i], inv, 12582912.0f));
+        const uint32_t code = (uint32_t)(b - kMagicBits + (QP + 1));
+        h[i / 8] |= (KvHalf<B>)code << (B * (i % 8));
+    }
+    return __fdiv_rn(g, qp);
+}
+
+// Stores lane li's 16 codes of the row at dst (D*B/8 bytes).  Every lane of the
+// warp calls it (3-bit lane pairs share a 12-byte group through a shuffle).
+template <int B>
+__device__ __forceinline__ void kv_store16(uint8_t* dst, int li, const KvHalf<B> (&h)[2], bool ok) {
+    if constexpr (B == 8) {  // 16 bytes per lane
+        if (ok)
+            *reinterpret_cast<uint4*>(dst + li * 16) =
+                make_uint4((uint32_t)h[0], (uint32_t)((uint64_t)h[0] >> 32), (uint32_t)h[1],
+                           (uint32_t)((uint64_t)h[1] >> 32));
+    } else if constexpr (B == 4) {  // 8 bytes per lane
+        if (ok) *reinterpret_cast<uint2*>(dst + li * 8) = make_uint2(h[0], h[1]);
+    } else if constexpr (B == 2) {  // 4 bytes per lane
+        if (ok) *reinterpret_cast<uint32_t*>(dst + li * 4) = h[0] | (h[1] << 16);
+    } else {  // B == 3: 48 bits per lane; a lane pair makes one 12-byte group
+        const uint64_t mine = (uint64_t)h[0] | ((uint64_t)h[1] << 24);
+        const uint64_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+        if (ok && (li & 1) == 0) {
+            uint32_t* d32 = reinterpret_cast<uint32_t*>(dst + (li >> 1) * 12);
+            d32[0] = (uint32_t)mine;
+            d32[1] = (uint32_t)(mine >> 32) | ((uint32_t)next << 16);
+            d32[2] = (uint32_t)(next >> 16);
+        }
+    }
+}
+
+// Loads lane li's 16 codes of the row at src: h as kv_quant16 leaves them.
+template <int B>
+__device__ __forceinline__ void kv_load16(const uint8_t* src, int li, KvHalf<B> (&h)[2]) {
+    if constexpr (B == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + li * 16);
+        h[0] = (uint64_t)v.x | ((uint64_t)v.y << 32);
+        h[1] = (uint64_t)v.z | ((uint64_t)v.w << 32);
+    } else if constexpr (B == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + li * 8);
+        h[0] = v.x;
+        h[1] = v.y;
+    } else if constexpr (B == 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(src + li * 4);
+        h[0] = v & 0xffffu;
+        h[1] = v >> 16;
+    } else {  // 48 bits at bit 48 * (li & 1) of the pair's 96
+        const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + (li >> 1) * 12) + (li & 1);
+        const uint64_t v = ((uint64_t)s32[0] | ((uint64_t)s32[1] << 32)) >> ((li & 1) * 16);
+        h[0] = (uint32_t)v & 0xffffffu;
+        h[1] = (uint32_t)(v >> 24) & 0xffffffu;
+    }
+}
+
+// Two fp32 -> a bf16 pair (low half = first), round to nearest even.
+__device__ __forceinline__ uint32_t f2_to_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Calls f(ic<D>, ic<bits>) for the cache's head size and code width.
+template <class F>
+hbl_status kv_dispatch(int D, int bits, F&& f) {
+    auto by_bits = [&](auto d) -> hbl_status {
+        switch (bits) {
+            case 2: return f(d, ic<2>{});
+            case 3: return f(d, ic<3>{});
+            case 4: return f(d, ic<4>{});
+            case 8: return f(d, ic<8>{});
+            default: return HBL_ERR_INVALID_ARG;
+        }
+    };
+    switch (D) {
+        case 32: return by_bits(ic<32>{});
+        case 64: return by_bits(ic<64>{});
+        case 128: return by_bits(ic<128>{});
+        case 256: return by_bits(ic<256>{});
+        default: return HBL_ERR_SHAPE;
+    }
+}
+
+// ------------------------------------------------------------ the paged batch
+
+// One sequence of the batch: rows [r0, r1) of the packed new rows, `len`
+// positions in all; row t stands at position len - (r1 - r0) + (t - r0) (negative
+// for rows that the length does not reach).  Descriptors outside their bounds
+// are clamped, so nothing out of range is ever addressed, and `bad` is set.
+struct KvSeq {
+    int r0, r1, len;
+    bool bad;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {
+    KvSeq s;
+    const int c0 = __ldg(kb.cu + b), c1 = __ldg(kb.cu + b + 1), n = __ldg(kb.lens + b);
+    s.r0 = min(max(c0, 0), kb.rows);
+    s.r1 = min(max(c1, s.r0), kb.rows);
+    const int64_t cap = (int64_t)kb.pages_per_seq * page_size;
+    s.len = (int)min((int64_t)max(n, 0), cap);
+    s.bad = s.r0 != c0 || s.r1 != c1 || s.len != n;
+    return s;
+}
+
+// The sequence of packed row t, found by the whole warp (every lane calls it
+// with the same t): the number of sequences whose rows end at or before t.
+// kb.num_seqs for a row behind the last sequence.
+__device__ __forceinline__ int kv_seq_of_row(const KvBatch& kb, int t) {
+    const int lane = threadIdx.x & 31;
+    int b = 0;
+    for (int i = 0; i < kb.num_seqs; i += 32) {
+        const bool before = i + lane < kb.num_seqs && __ldg(kb.cu + i + lane + 1) <= t;
+        b += __popc(__ballot_sync(0xffffffffu, before));
+    }
+    return b;
+}
+
+// The page that holds position pos of sequence b, or -1 if the block table names
+// a page outside the pool.  0 <= pos < the sequence's clamped length.
+__device__ __forceinline__ int kv_page(const KvBatch& kb, int num_pages, int b, int page_index) {
+    const int page = __ldg(kb.table + (int64_t)b * kb.pages_per_seq + page_index);
+    return (unsigned)page < (unsigned)num_pages ? page : -1;
+}
+
+}  // namespace hbl

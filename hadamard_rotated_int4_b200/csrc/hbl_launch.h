@@ -94,6 +94,46 @@ hbl_status launch_rotate_weights(const float* W, const float* signs, int N, int 
 hbl_status launch_kv_quant(const uint16_t* X, int64_t rows, int D, int bits, float eps,
                            uint8_t* codes, float* scales, cudaStream_t stream, int num_sms);
 
+// The paged KV cache and a packed batch over it, as the kernels take them (the
+// public hbl_kv_cache / hbl_kv_batch with their fields checked).
+struct KvCache {
+    uint8_t* kc;   // [pages][heads][page_size][D*bits/8]
+    float* ks;     // [pages][heads][page_size]
+    uint8_t* vc;
+    float* vs;
+    int num_pages, page_size, heads, D, bits;
+};
+struct KvBatch {
+    const int32_t* cu;     // [num_seqs + 1]
+    const int32_t* lens;   // [num_seqs]
+    const int32_t* table;  // [num_seqs][pages_per_seq]
+    int num_seqs, pages_per_seq, rows;
+};
+// K11: quantise new K/V rows into their pages; dequantise rows out of them.
+struct KvStates {  // strides in elements
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_row, k_head, v_row, v_head;
+};
+hbl_status launch_kv_cache_write(const KvCache& c, const KvBatch& b, const KvStates& x, float eps,
+                                 int32_t* status, cudaStream_t stream, int num_sms);
+hbl_status launch_kv_cache_read(const KvCache& c, const KvBatch& b, void* k_out, void* v_out,
+                                bool fp32, int32_t* status, cudaStream_t stream, int num_sms);
+// K12: attention of the new rows over the cache.
+struct KvAttn {
+    const uint16_t* q;
+    uint16_t* o;
+    float* lse;  // nullable
+    int64_t q_row, q_head, o_row, o_head;
+    int heads, group;  // query heads, query heads per cached head
+    int max_rows, max_kv;
+    float scale;
+    int causal, window;
+};
+size_t kv_attention_workspace(const KvCache& c, const KvBatch& b, const KvAttn& a);
+hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn& a, void* ws,
+                               int32_t* status, cudaStream_t stream, int num_sms);
+
 // Self-test of the bounded-wait failure path (see k9_selftest.cu).
 hbl_status launch_bounded_wait_probe(int arrive, int timeout_us, int32_t* status,
                                      cudaStream_t stream);

@@ -1,0 +1,227 @@
+// k11_kv_cache.cu -- the paged low-bit KV cache: new K/V rows quantised into
+// their pages, and rows dequantised out of them.
+//
+// One head row (one token's D values of one head) is coded as K5 codes it:
+//   gamma = max|x|;  inv = Qp / (gamma + eps);  u = rhe(x * inv) + 2^(b-1);
+//   scale = gamma / Qp;  value = (u - 2^(b-1)) * scale
+// and stored at row (page * heads + head) * page_size + slot of the codes and
+// scales, page = block_table[seq][pos / page_size], slot = pos % page_size.  A
+// head's rows of one page are contiguous, so the attention that reads them
+// streams whole pages of its head.
+//
+// Both kernels are bound by HBM at large batches and by launch latency at one
+// decoding step.  A warp takes one token and 1..kSteps steps of its 2 * heads
+// head rows (K heads, then V heads; D/16 lanes a row, 16 values a lane): the
+// token's sequence, position and page are found once per warp, by one load and
+// ballot per 32 sequences instead of a chain of dependent loads.
+#include "hbl_kv.cuh"
+
+namespace hbl {
+namespace k11 {
+
+constexpr int kThreads = 256;
+constexpr int kSteps = 4;  // most steps of one warp task
+
+struct Task {
+    int tasks_per_row;  // warp tasks of one token
+    int per_task;       // head rows of one task
+    int64_t tasks;
+};
+
+// Where the token of this warp's task stands in the cache.
+struct Place {
+    int64_t base;  // (page * heads) * page_size + slot
+    bool in_seq;   // the row belongs to a sequence of the batch
+    bool ok;       // and has a place in a page of the pool
+};
+__device__ __forceinline__ Place place_of(const KvCache& c, const KvBatch& kb, int t,
+                                          int32_t* status) {
+    Place p;
+    p.base = 0;
+    p.in_seq = p.ok = false;
+    const int b = kv_seq_of_row(kb, t);
+    if (b >= kb.num_seqs) return p;  // behind the last sequence
+    const KvSeq s = kv_seq(kb, c.page_size, b);
+    const int pos = s.len - (s.r1 - s.r0) + (t - s.r0);
+    bool bad = s.bad;
+    p.in_seq = t >= s.r0 && t < s.r1;
+    if (p.in_seq && pos >= 0) {
+        const int pi = pos / c.page_size;
+        const int page = kv_page(kb, c.num_pages, b, pi);
+        if (page >= 0) {
+            p.base = (int64_t)page * c.heads * c.page_size + (pos - pi * c.page_size);
+            p.ok = true;
+        } else {
+            bad = true;
+        }
+    }
+    if (bad && (threadIdx.x & 31) == 0) report_status(status, HBL_ERR_INVALID_ARG);
+    return p;
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(kThreads) write_kernel(KvCache c, KvBatch kb, KvStates x,
+                                                         float eps, Task k, int32_t* status) {
+    constexpr int LPR = D / kKvVpl;
+    constexpr int RPW = 32 / LPR;
+    constexpr int ROW_BYTES = D * B / 8;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
+    const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
+    for (int64_t task = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; task < k.tasks;
+         task += warps) {
+        const int t = (int)(task / k.tasks_per_row);
+        const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
+        const int last = min(first + k.per_task, 2 * c.heads);
+        uint4 raw[2][2];
+        auto load = [&](int r, uint4 (&v)[2]) {  // head row r: K heads, then V heads
+            const bool isv = r >= c.heads;
+            const uint16_t* src = isv ? x.v + (int64_t)t * x.v_row + (int64_t)(r - c.heads) * x.v_head
+                                      : x.k + (int64_t)t * x.k_row + (int64_t)r * x.k_head;
+            const uint4* s = reinterpret_cast<const uint4*>(src + li * kKvVpl);
+            v[0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
+            v[1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
+        };
+        load(first + sub, raw[0]);  // the rows load while the token's place is found
+        const Place p = place_of(c, kb, t, status);
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {
+            const int r0 = first + step * RPW;
+            if (r0 >= last) break;
+            if (step + 1 < kSteps && r0 + RPW < last) load(r0 + RPW + sub, raw[(step + 1) & 1]);
+            const int r = r0 + sub;
+            KvHalf<B> h[2];
+            const float scale = kv_quant16<D, B>(raw[step & 1], eps, h);
+            const bool ok = p.ok && r < last, isv = r >= c.heads;
+            const int64_t row = p.base + (int64_t)(isv ? r - c.heads : r) * c.page_size;
+            kv_store16<B>((isv ? c.vc : c.kc) + row * ROW_BYTES, li, h, ok);
+            if (ok && li == 0) (isv ? c.vs : c.ks)[row] = scale;
+        }
+    }
+}
+
+// value = (u - 2^(B-1)) * scale, one fp32 rounding, then one to bf16.
+template <int B>
+__device__ __forceinline__ void values16(const KvHalf<B> (&h)[2], float scale, float (&v)[16]) {
+    constexpr int kMask = (1 << B) - 1, kHalf = 1 << (B - 1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int u = (int)(h[i / 8] >> (B * (i % 8))) & kMask;
+        v[i] = __fmul_rn((float)(u - kHalf), scale);
+    }
+}
+
+template <int D, int B, bool F32>
+__global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, KvBatch kb, void* k_out,
+                                                        void* v_out, Task k, int32_t* status) {
+    constexpr int LPR = D / kKvVpl;
+    constexpr int RPW = 32 / LPR;
+    constexpr int ROW_BYTES = D * B / 8;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
+    const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
+    for (int64_t task = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; task < k.tasks;
+         task += warps) {
+        const int t = (int)(task / k.tasks_per_row);
+        const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
+        const int last = min(first + k.per_task, 2 * c.heads);
+        const Place p = place_of(c, kb, t, status);
+        if (!p.in_seq) continue;  // left as it was
+        KvHalf<B> h[kSteps][2];
+        float scale[kSteps];
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {  // every load in flight before the first use
+            const int r = first + step * RPW + sub;
+            const bool isv = r >= c.heads;
+            h[step][0] = h[step][1] = 0;
+            scale[step] = 0.f;
+            if (r < last && p.ok) {
+                const int64_t row = p.base + (int64_t)(isv ? r - c.heads : r) * c.page_size;
+                kv_load16<B>((isv ? c.vc : c.kc) + row * ROW_BYTES, li, h[step]);
+                scale[step] = (isv ? c.vs : c.ks)[row];
+            }
+        }
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {
+            const int r = first + step * RPW + sub;
+            if (r >= last) continue;
+            const bool isv = r >= c.heads;
+            float v[16];
+            values16<B>(h[step], scale[step], v);
+            const int64_t at =
+                ((int64_t)t * c.heads + (isv ? r - c.heads : r)) * D + li * kKvVpl;
+            if constexpr (F32) {
+                float4* dst = reinterpret_cast<float4*>((float*)(isv ? v_out : k_out) + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(v[2 * i], v[2 * i + 1]);
+                uint4* dst = reinterpret_cast<uint4*>((uint16_t*)(isv ? v_out : k_out) + at);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+    }
+}
+
+// Few head rows in all: one step a warp, for the most warps in flight.  Many:
+// kSteps steps, which share the search for the token's page.
+template <int D>
+static Task plan(const KvCache& c, const KvBatch& b, int num_sms, unsigned* grid) {
+    constexpr int RPW = 32 / (D / kKvVpl);
+    const int64_t head_rows = 2ll * c.heads;
+    Task k;
+    int steps = kSteps;
+    while (steps > 1 && (int64_t)b.rows * ((head_rows + steps * RPW - 1) / (steps * RPW)) <
+                            (int64_t)num_sms * 32)
+        steps >>= 1;
+    k.per_task = steps * RPW;
+    k.tasks_per_row = (int)((head_rows + k.per_task - 1) / k.per_task);
+    k.tasks = (int64_t)b.rows * k.tasks_per_row;
+    const int64_t ctas = (k.tasks + kThreads / 32 - 1) / (kThreads / 32);
+    *grid = (unsigned)(ctas < (int64_t)num_sms * 64 ? ctas : (int64_t)num_sms * 64);
+    return k;
+}
+
+static hbl_status done() { return cudaGetLastError() == cudaSuccess ? HBL_OK : HBL_ERR_CUDA; }
+
+template <int D, int B>
+static hbl_status write_one(const KvCache& c, const KvBatch& b, const KvStates& x, float eps,
+                            int32_t* status, cudaStream_t s, int sms) {
+    unsigned grid;
+    const Task k = plan<D>(c, b, sms, &grid);
+    write_kernel<D, B><<<grid, kThreads, 0, s>>>(c, b, x, eps, k, status);
+    return done();
+}
+template <int D, int B>
+static hbl_status read_one(const KvCache& c, const KvBatch& b, void* ko, void* vo, bool fp32,
+                           int32_t* status, cudaStream_t s, int sms) {
+    unsigned grid;
+    const Task k = plan<D>(c, b, sms, &grid);
+    if (fp32)
+        read_kernel<D, B, true><<<grid, kThreads, 0, s>>>(c, b, ko, vo, k, status);
+    else
+        read_kernel<D, B, false><<<grid, kThreads, 0, s>>>(c, b, ko, vo, k, status);
+    return done();
+}
+
+}  // namespace k11
+
+hbl_status launch_kv_cache_write(const KvCache& c, const KvBatch& b, const KvStates& x, float eps,
+                                 int32_t* status, cudaStream_t stream, int num_sms) {
+    return kv_dispatch(c.D, c.bits, [&](auto d, auto bits) {
+        return k11::write_one<decltype(d)::value, decltype(bits)::value>(c, b, x, eps, status,
+                                                                         stream, num_sms);
+    });
+}
+
+hbl_status launch_kv_cache_read(const KvCache& c, const KvBatch& b, void* k_out, void* v_out,
+                                bool fp32, int32_t* status, cudaStream_t stream, int num_sms) {
+    return kv_dispatch(c.D, c.bits, [&](auto d, auto bits) {
+        return k11::read_one<decltype(d)::value, decltype(bits)::value>(c, b, k_out, v_out, fp32,
+                                                                        status, stream, num_sms);
+    });
+}
+
+}  // namespace hbl

@@ -23,17 +23,14 @@
 // row; each warp keeps U steps of loads in flight.
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
-#include "hbl_internal.cuh"
-#include "hbl_launch.h"
+#include "hbl_kv.cuh"
 
 namespace hbl {
 namespace k5 {
 
 constexpr int kThreads = 256;
 constexpr int U = 2;     // row steps per warp with their loads in flight together
-constexpr int VPL = 16;  // values per lane
+constexpr int VPL = kKvVpl;  // values per lane
 
 template <int D, int B>
 __global__ void __launch_bounds__(kThreads) kv_quant_kernel(const uint16_t* __restrict__ X,
@@ -43,13 +40,10 @@ __global__ void __launch_bounds__(kThreads) kv_quant_kernel(const uint16_t* __re
     constexpr int LPR = D / VPL;     // lanes per row
     constexpr int RPW = 32 / LPR;    // rows per warp step
     constexpr int ROW_BYTES = D * B / 8;
-    constexpr int QP = (1 << (B - 1)) - 1;
-    constexpr int32_t kMagicBits = 0x4B400000;  // 1.5 * 2^23
     const int lane = threadIdx.x & 31;
     const int sub = lane / LPR, li = lane % LPR;
     const int64_t warp0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
     const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-    const float qp = (float)QP;
 
     for (int64_t base = warp0 * (RPW * U); base < rows; base += nwarps * (RPW * U)) {
         uint4 raw[U][2];
@@ -63,59 +57,11 @@ __global__ void __launch_bounds__(kThreads) kv_quant_kernel(const uint16_t* __re
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = base + u * RPW + sub;
-            float x[VPL];
-            {
-                const uint32_t w[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w,
-                                       raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = bf16x2_to_f2(w[i]);
-                    x[2 * i] = f.x;
-                    x[2 * i + 1] = f.y;
-                }
-            }
-            float g = 0.f;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) g = fmaxf(g, fabsf(x[i]));
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-            const float den = __fadd_rn(g, eps);
-            const float inv = den > 0.f ? __fdiv_rn(qp, den) : 0.f;
-            // 16 codes of this lane, code i at bits [B*i, B*i + B) of a 16*B-bit
-            // field (two 32-bit halves of 8 codes each).  No clamp is needed:
-            // |x| <= gamma, so |x * inv| <= Qp * gamma / (gamma + eps) up to the
-            // rounding of inv (well under half a unit), and rounding to the
-            // nearest integer stays within [-Qp, Qp].
-            using Half = typename std::conditional<(8 * B <= 32), uint32_t, uint64_t>::type;
-            Half h[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int32_t b = __float_as_int(__fmaf_rn(x[i], inv, 12582912.0f));
-                const uint32_t code = (uint32_t)(b - kMagicBits + (QP + 1));
-                h[i / 8] |= (Half)code << (B * (i % 8));
-            }
+            KvHalf<B> h[2];
+            const float scale = kv_quant16<D, B>(raw[u], eps, h);
             const bool ok = row < rows;
-            uint8_t* dst = codes + row * ROW_BYTES;
-            if constexpr (B == 8) {  // 16 bytes per lane
-                if (ok)
-                    *reinterpret_cast<uint4*>(dst + li * 16) =
-                        make_uint4((uint32_t)h[0], (uint32_t)((uint64_t)h[0] >> 32), (uint32_t)h[1],
-                                   (uint32_t)((uint64_t)h[1] >> 32));
-            } else if constexpr (B == 4) {  // 8 bytes per lane
-                if (ok) *reinterpret_cast<uint2*>(dst + li * 8) = make_uint2(h[0], h[1]);
-            } else if constexpr (B == 2) {  // 4 bytes per lane
-                if (ok) *reinterpret_cast<uint32_t*>(dst + li * 4) = h[0] | (h[1] << 16);
-            } else {  // B == 3: 48 bits per lane; a lane pair makes one 12-byte group
-                const uint64_t mine = (uint64_t)h[0] | ((uint64_t)h[1] << 24);
-                const uint64_t next = __shfl_down_sync(0xffffffffu, mine, 1);
-                if (ok && (li & 1) == 0) {
-                    uint32_t* d32 = reinterpret_cast<uint32_t*>(dst + (li >> 1) * 12);
-                    d32[0] = (uint32_t)mine;
-                    d32[1] = (uint32_t)(mine >> 32) | ((uint32_t)next << 16);
-                    d32[2] = (uint32_t)(next >> 16);
-                }
-            }
-            if (ok && li == 0) scales[row] = __fdiv_rn(g, qp);
+            kv_store16<B>(codes + row * ROW_BYTES, li, h, ok);
+            if (ok && li == 0) scales[row] = scale;
         }
     }
 }

@@ -328,6 +328,95 @@ HBL_API hbl_status hbl_rotate_weights(const float* W, const float* signs, int N,
 HBL_API hbl_status hbl_kv_quant(const uint16_t* X, int64_t rows, int D, int bits, float eps,
                                 uint8_t* codes, float* scales, int32_t* dev_status, void* stream);
 
+/* -------------------------------------------------- paged low-bit KV cache
+ * The cache that hbl_kv_quant's codes are for, and the attention that reads it.
+ * Token t, cached head h: D values coded as hbl_kv_quant codes a row (`bits`
+ * bits a value, one fp32 scale), value (u - 2^(bits-1)) * scale.  Pages hold
+ * page_size positions of one sequence, all heads:
+ *   codes  [num_pages][num_kv_heads][page_size][D*bits/8] bytes
+ *   scales [num_pages][num_kv_heads][page_size]           fp32
+ * Position p of sequence b is slot p % page_size of page
+ * block_table[b][p / page_size].  head_dim D in {32, 64, 128, 256}; bits in
+ * {2, 3, 4, 8}; page_size a multiple of 16 in [16, 65536]; 1 <= num_kv_heads
+ * <= 65535; pages_per_seq * page_size < 2^31. */
+typedef struct {
+    uint8_t* k_codes;
+    float* k_scales;
+    uint8_t* v_codes;
+    float* v_scales;
+    int num_pages, page_size, num_kv_heads, head_dim, bits;
+} hbl_kv_cache;
+
+/* A packed batch of num_seqs sequences over a cache (device arrays, 4-byte
+ * aligned; their values are read on the device, so a captured graph replays
+ * with new ones).  Rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of `rows` packed
+ * rows are sequence b's; kv_lens[b] is its length including them, so its row i
+ * stands at position kv_lens[b] - (cu_seqlens[b+1] - cu_seqlens[b]) + i.  A row
+ * at a negative position has no place: it is not written, reads as zeros, and
+ * with a causal mask sees no key.  Rows before cu_seqlens[0] or behind
+ * cu_seqlens[num_seqs] belong to no sequence: no call writes their results.
+ * cu_seqlens must not decrease and must stay in [0, rows]; 0 <= kv_lens[b] <=
+ * pages_per_seq * page_size; the first ceil(kv_lens[b] / page_size) entries of
+ * block_table[b] name pages of the cache.  Violations are memory-safe: the
+ * offending rows, positions or pages are left out and dev_status (if given)
+ * becomes HBL_ERR_INVALID_ARG.  Entries past a sequence's length are not used. */
+typedef struct {
+    const int32_t* cu_seqlens;  /* [num_seqs + 1] */
+    const int32_t* kv_lens;     /* [num_seqs] */
+    const int32_t* block_table; /* [num_seqs][pages_per_seq] */
+    int num_seqs, pages_per_seq, rows;
+} hbl_kv_batch;
+
+/* Quantises K and V (bf16, after RoPE; row t, head h at t * row_stride + h *
+ * head_stride elements, D contiguous; strides multiples of 8) into the batch's
+ * positions, with hbl_kv_quant's formulas and eps.  The batch's positions must
+ * not share a page slot (two sequences may share pages that neither writes). */
+HBL_API hbl_status hbl_kv_cache_write(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                                      const uint16_t* K, int64_t k_row_stride,
+                                      int64_t k_head_stride, const uint16_t* V,
+                                      int64_t v_row_stride, int64_t v_head_stride, float eps,
+                                      int32_t* dev_status, void* stream);
+
+/* Dequantises the batch's positions: K_out, V_out [rows x num_kv_heads x D],
+ * bf16 (out_fp32 0: the fp32 value rounded to nearest even) or fp32 (1). */
+HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                                     void* K_out, void* V_out, int out_fp32, int32_t* dev_status,
+                                     void* stream);
+
+/* Attention of the batch's rows over everything their sequences have cached
+ * (their own positions among it: write them first).  Query head j reads cached
+ * head j / (num_heads / num_kv_heads).  For row t at position p, head j:
+ *   s_i = scale * (Q[t][j] . K_i) over the visible positions i,
+ *   O[t][j] = sum_i softmax(s)_i * V_i,  lse[t][j] = ln sum_i exp(s_i)
+ * with i visible if i < kv_len, (causal) i <= p and (window w > 0) i > p - w.
+ * A row that sees nothing has O = 0 and lse = -inf.  Stored bytes past a
+ * sequence's length are never used, whatever they hold.
+ * Q, O: bf16, strided as K above (O must not overlap Q); lse: fp32
+ * [rows x num_heads] or NULL.  num_heads a multiple of num_kv_heads, at most
+ * 65535.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
+ * past it are left out and reported); max_kv: about the longest sequence (0:
+ * unknown), a hint that only speed depends on.  Products are exact, sums and
+ * softmax are fp32; the probabilities that weight V are rounded to fp16. */
+typedef struct {
+    const uint16_t* Q;
+    int64_t q_row_stride, q_head_stride;
+    uint16_t* O;
+    int64_t o_row_stride, o_head_stride;
+    float* lse;
+    int num_heads, max_rows, max_kv;
+    float scale;
+    int causal, window;
+} hbl_kv_attn;
+
+/* Workspace bytes of hbl_kv_attention for these sizes (only they are read, no
+ * pointer).  Calls that may run at the same time need a workspace each. */
+HBL_API hbl_status hbl_kv_attention_workspace(const hbl_kv_cache* cache,
+                                              const hbl_kv_batch* batch, const hbl_kv_attn* attn,
+                                              size_t* bytes);
+HBL_API hbl_status hbl_kv_attention(const hbl_kv_cache* cache, const hbl_kv_batch* batch,
+                                    const hbl_kv_attn* attn, void* ws, size_t ws_bytes,
+                                    int32_t* dev_status, void* stream);
+
 /* --------------------------------------------------- expanded-weight GEMM
  * For large token batches the tensor-core GEMM reads the ternary weights as
  * one signed byte each (tcgen05 has no integer MMA narrower than 8 bits);
