@@ -1,0 +1,11 @@
+// k13_kv_decode_d256.cu -- the few-rows attention kernel for head size 256.
+#include "k13_kv_decode.cuh"
+
+namespace hbl {
+namespace k13 {
+hbl_status launch_d256(const KvCache& c, const KvBatch& b, const KvAttn& a, const k12::Plan& pl,
+                     float* part, int32_t* status, cudaStream_t stream) {
+    return launch_d<256>(c, b, a, pl, part, status, stream);
+}
+}  // namespace k13
+}  // namespace hbl
