@@ -14,11 +14,11 @@
 namespace hbl {
 namespace k12 {
 
-// How the launch is split; made on the host from sizes alone (make_plan).
+// How the launch is split; made on the host from sizes alone (few_plan, chunk_plan).
 struct Plan {
     int block_rows;  // head rows of a CTA
     int row_blocks;  // CTAs to a sequence's head rows
-    int few_rows;    // sequences with more head rows than this are not this kernel's
+    int min_rows, max_rows;  // the kernel takes sequences with so many head rows
     int splits;      // most ranges of positions of one row block
     int quantum;     // positions of a range (more where `splits` ranges would not reach)
     uint32_t page_mul, page_shift;  // x / page_size = (mulhi(x, mul) + x) >> shift, x < 2^31
@@ -107,9 +107,6 @@ __device__ __forceinline__ void store_row(const KvAttn& a, const Rows& s, int h,
             L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
 }
 
-// Host: ranges for `ctas` row blocks over `span` positions.
-Plan make_plan(const KvCache& c, const KvBatch& b, const KvAttn& a);
-
 }  // namespace k12
 
 namespace k13 {
@@ -123,4 +120,16 @@ hbl_status launch_d128(const KvCache&, const KvBatch&, const KvAttn&, const k12:
 hbl_status launch_d256(const KvCache&, const KvBatch&, const KvAttn&, const k12::Plan&, float* part,
                        int32_t* status, cudaStream_t);
 }  // namespace k13
+
+namespace k14 {
+// Chunks: per head size, in files of their own (k14_kv_chunk_d*.cu).
+hbl_status launch_d32(const KvCache&, const KvBatch&, const KvAttn&, const k12::Plan&, float* part,
+                      int32_t* status, cudaStream_t);
+hbl_status launch_d64(const KvCache&, const KvBatch&, const KvAttn&, const k12::Plan&, float* part,
+                      int32_t* status, cudaStream_t);
+hbl_status launch_d128(const KvCache&, const KvBatch&, const KvAttn&, const k12::Plan&, float* part,
+                       int32_t* status, cudaStream_t);
+hbl_status launch_d256(const KvCache&, const KvBatch&, const KvAttn&, const k12::Plan&, float* part,
+                       int32_t* status, cudaStream_t);
+}  // namespace k14
 }  // namespace hbl

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
     if (s.bad && split == 0 && rb == 0 && h == 0 && threadIdx.x == 0)
         report_status(status, HBL_ERR_INVALID_ARG);
     const int nr = s.n * a.group;  // this sequence's rows on this head
-    if (nr > pl.few_rows || rb * R >= nr) return;
+    if (nr < pl.min_rows || nr > pl.max_rows || rb * R >= nr) return;
     const k12::Range rg = k12::range_of(a, s, rb * R, min(nr, rb * R + R) - 1);
     const k12::Split sp = k12::split_of(pl, rg, split);
     if (split >= max(sp.count, 1)) return;

@@ -1,0 +1,823 @@
+// k14_kv_chunk.cuh -- attention of a chunk of new rows over the paged low-bit
+// cache, on the tcgen05 tensor cores.
+//
+// The mathematics is k13_kv_decode.cuh's: with integer codes k, v and scales,
+//   x_i = scale * log2(e) * sk_i * (q . k_i) + log2(sv_i),
+//   O = sum_i 2^(x_i - m) v_i / sum_i 2^(x_i - m) / sv_i
+// so both products run on exact integers (bf16 keys against bf16 queries, fp16
+// values against fp16 weights) and the scales cost one packed fma per pair of
+// scores.  The reference point m follows the running maximum only when a
+// score passes it by more than 2^8 (weights stay below 2^14 in fp16): the
+// accumulator in tensor memory is rescaled a few times a row, not every tile.
+//
+// One CTA: one sequence, cached head and 2 x 128 head rows (128 at D = 256),
+// and a range of positions in tiles of KT.  Sixteen warps:
+//   0..7    softmax, four warps to each 128 rows: scores out of tensor memory,
+//           weights back into it in the scores' place
+//   8..14   widen K and V codes from HBM straight into swizzled operand tiles
+//           (two stages each) and lay out the tiles' scales
+//   15      one thread issues the MMAs: S = Q K^T (both operands in shared
+//           memory), O += P V (P in tensor memory, V read down its rows, which
+//           is the transposed operand that the second product needs)
+// While one set of rows is in its softmax the tensor core works for the other.
+//
+// What bounds it: a tile of 128 positions is 4 * 128^3 * 2 products for the
+// two row sets, 2048 tensor cycles at D = 128, and 2 * 128 * 128 exponentials,
+// 2048 cycles of the 16-a-cycle special-function units: both at once at best.
+// Shared memory is nearly as busy (1536 cycles of MMA operand reads, 512 of
+// operand tiles stored), which is why scores leave tensor memory in the
+// 16x256b shape: a thread then needs a quarter of a tile's scales, not all.
+//
+// D order.  Widening gives codes in pairs (i, i + C/2) of C; queries are laid
+// out in the same order, and O's columns are put back when it is stored.
+#pragma once
+
+#include "hbl_kv_codes.cuh"
+#include "hbl_tmem.cuh"
+#include "k12_kv_attention.cuh"
+
+namespace hbl {
+namespace k14 {
+
+using k12::Plan;
+
+constexpr int kThreads = 512;
+constexpr int kConv = 7;             // widening warps
+constexpr int kConvWarp0 = 8, kMmaWarp = 15;
+constexpr float kShift = 6.f;        // weights are held times 2^6 ...
+constexpr float kLazy = 8.f;         // ... and may pass the reference by 2^8
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kScaleStages = 4;
+
+template <int D>
+struct Tile {
+    static constexpr int NQ = D == 256 ? 1 : 2;       // sets of 128 rows
+    static constexpr int KT = D == 256 ? 64 : 128;    // positions of a tile
+    static constexpr int kPanels = D >= 64 ? D / 64 : 1;  // 128-byte panels of a row
+    static constexpr int kSBuf = 2;                   // score buffers in tensor memory
+    static constexpr uint32_t kOCol = kSBuf * KT;     // first accumulator column
+    static constexpr int kQ = NQ * 128 * kPanels * 128;  // bytes
+    static constexpr int kStage = KT * kPanels * 128;    // one operand tile
+    static constexpr int kScale = KT * 12;               // (ck, ck, lv, lv) a pair, then 1/sv
+    static constexpr int kBars = 256;
+    static constexpr int kUnits = KT * (D / 32) / 32;    // warp units of 32 x 32 codes
+    static constexpr int kMine = (kUnits + kConv - 1) / kConv;
+    static constexpr int kSmem = kQ + 4 * kStage + kScaleStages * kScale + kBars + 1024;
+};
+
+// K-major (queries, keys) and row-major-down (values) descriptors of operand
+// tiles in 128-byte swizzled panels: eight rows of 128 bytes to an atom.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// leading offset: from one panel of 64 columns to the next
+__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t panel_bytes) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(panel_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: D fp32 (bits 4-5 = 1), A and B types (bits 7-9, 10-12: 0 fp16, 1
+// bf16), B transposed (bit 16), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t idesc(bool bf16, bool b_mn, int N) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t accum) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t accum) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t mbar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_alloc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dealloc() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Bounded wait; on expiry (here or, through the flag, anywhere in the CTA) false.
+// one(): by a single thread.  all(): by a whole warp, whose lanes leave it
+// together -- the tensor-memory instructions that follow need the warp
+// converged, and lanes that poll for themselves come out one after another.
+struct Waiter {
+    volatile int* abort_flag;
+    int32_t* status;
+    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, one(bar, parity));
+    }
+    __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const {
+        if (mbar_test_parity(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        while (true) {
+            if (mbar_test_parity(bar, parity)) return true;
+            if (*abort_flag) return false;
+            if (global_ns() - t0 > kTimeoutNs) {
+                *abort_flag = 1;
+                report_status(status, HBL_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+};
+
+// A lane's place in a unit of 32 lanes x 32 codes: eight neighbouring lanes take
+// four rows and two groups of a row, so that their 16-byte stores fall into
+// different banks of the swizzled tile.
+template <int D>
+struct Lane {
+    static constexpr int kGroups = D / 32;          // groups of 32 codes in a row
+    static constexpr int kRows = 32 / kGroups;      // rows of a unit
+    int row, group;
+    __device__ __forceinline__ explicit Lane(int lane) {
+        if constexpr (kGroups == 1) {
+            row = lane;
+            group = 0;
+        } else {
+            const int lo = lane & 1, k = (lane >> 1) & 3, rest = lane >> 3;
+            constexpr int kHigh = kGroups / 2;  // 1, 2, 4
+            group = (rest % kHigh) * 2 + lo;
+            row = (rest / kHigh) * 4 + k;
+        }
+    }
+};
+// Byte offset of 16-byte chunk q (0..3) of a group in a tile of `rows` rows.
+__device__ __forceinline__ uint32_t chunk_at(int rows, int row, int group, int q) {
+    const int chunk = (group & 1) * 4 + q;
+    return (uint32_t)((group >> 1) * rows * 128 + row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+// 32 codes (B words) -> 16 pairs, as bf16 or fp16.
+template <int B, bool BF16>
+__device__ __forceinline__ void widen32(const uint32_t (&raw)[B], uint32_t (&out)[16]) {
+    constexpr int H = kKvHalfCodes<B>, W = 16 / H;
+    uint32_t w[W];
+    if constexpr (B == 3) {
+        w[0] = kv_spread3(raw[0]);
+        w[1] = kv_spread3(__funnelshift_r(raw[0], raw[1], 24));
+        w[2] = kv_spread3(__funnelshift_r(raw[1], raw[2], 16));
+        w[3] = kv_spread3(raw[2] >> 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = raw[i];
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        uint32_t p[H];
+        if constexpr (BF16)
+            kv_widen_bf16<B, H>(w[i], p);
+        else
+            kv_widen_f16<B, H>(w[i], p);
+#pragma unroll
+        for (int k = 0; k < H; ++k) out[H * i + k] = p[k];
+    }
+}
+// Within a group of 32: the value at place n of the order that widening gives.
+template <int B>
+__host__ __device__ constexpr int place_of(int n) {
+    const int H = kKvHalfCodes<B>, p = n / 2;
+    return p / H * 2 * H + p % H + (n & 1) * H;
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch kb, KvAttn a,
+                                                            Plan pl, float* part,
+                                                            int32_t* status) {
+    using T = Tile<D>;
+    constexpr int KT = T::KT, NQ = T::NQ;
+    constexpr int ROW_BYTES = D * B / 8;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_addr(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_s - raw_s);
+    const uint32_t q_s = base_s, k_s = q_s + T::kQ, v_s = k_s + 2 * T::kStage;
+    const uint32_t sc_s = v_s + 2 * T::kStage, bar_s = sc_s + kScaleStages * T::kScale;
+    uint8_t* bar_p = base + (bar_s - base_s);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_p + 200);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_p + 204);
+    auto kfull = [&](int s) { return bar_s + 8u * s; };
+    auto kempty = [&](int s) { return bar_s + 8u * (2 + s); };
+    auto vfull = [&](int s) { return bar_s + 8u * (4 + s); };
+    auto vempty = [&](int s) { return bar_s + 8u * (6 + s); };
+    auto scfull = [&](int s) { return bar_s + 8u * (8 + s); };
+    auto scempty = [&](int s) { return bar_s + 8u * (12 + s); };
+    auto sfull = [&](int s) { return bar_s + 8u * (16 + s); };
+    auto pfull = [&](int s) { return bar_s + 8u * (18 + s); };
+    auto ofull = [&](int s) { return bar_s + 8u * (20 + s); };
+    const uint32_t qfull = bar_s + 8u * 22, drain = bar_s + 8u * 23;
+
+    // ---- which rows, which positions: the longest row blocks start first
+    const int per_block = kb.num_seqs * pl.splits;
+    const int rb = pl.row_blocks - 1 - (int)(blockIdx.x / per_block);
+    const int b = (int)(blockIdx.x % per_block) / pl.splits;
+    const int split = (int)(blockIdx.x % per_block) % pl.splits, h = (int)blockIdx.y;
+    const k12::Rows s = k12::rows_of(kb, c.page_size, a, b);
+    if (s.bad && split == 0 && rb == 0 && h == 0 && threadIdx.x == 0)
+        report_status(status, HBL_ERR_INVALID_ARG);
+    const int nr = s.n * a.group, row0 = rb * 128 * NQ;
+    if (nr < pl.min_rows || nr > pl.max_rows || row0 >= nr) return;
+    const k12::Range rg = k12::range_of(a, s, row0, min(nr, row0 + 128 * NQ) - 1);
+    const k12::Split sp = k12::split_of(pl, rg, split);
+    if (split >= max(sp.count, 1)) return;
+    pdl_launch_dependents();
+    const int tiles = sp.count == 0 ? 0 : (sp.end - sp.begin + KT - 1) / KT;
+    const int sets = NQ == 2 && nr - row0 > 128 ? 2 : 1;  // row sets that have rows
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init_count(kfull(i), kConv);
+            mbar_init_count(kempty(i), 1);
+            mbar_init_count(vfull(i), kConv);
+            mbar_init_count(vempty(i), 1);
+            mbar_init_count(sfull(i), 1);
+            mbar_init_count(pfull(i), 4);
+            mbar_init_count(ofull(i), 1);
+        }
+        for (int i = 0; i < kScaleStages; ++i) {
+            mbar_init_count(scfull(i), 1);
+            mbar_init_count(scempty(i), 4 * sets);
+        }
+        mbar_init_count(qfull, 4 * sets);
+        mbar_init_count(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_addr(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Waiter wait{abort_flag, status};
+
+    if (warp < 8) {
+        // ================= softmax
+        reg_alloc<184>();
+        const int set = warp >> 2, quarter = warp & 3, g = lane >> 2, t = lane & 3;
+        if (set < sets) {
+            // ---- this set's queries into the operand layout
+            const Lane<D> ql(lane);
+            const uint32_t qbase = q_s + set * 128 * T::kPanels * 128;
+            constexpr int kUnits = 128 / Lane<D>::kRows;
+#pragma unroll 1
+            for (int u = quarter; u < kUnits; u += 4) {
+                const int row = u * Lane<D>::kRows + ql.row, r = row0 + set * 128 + row;
+                uint32_t raw[16], out[16];
+                const int i = r / a.group;
+                const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
+                                      (int64_t)(h * a.group + (r - i * a.group)) * a.q_head +
+                                      ql.group * 32;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 v = r < nr ? reinterpret_cast<const uint4*>(src)[k]
+                                           : make_uint4(0, 0, 0, 0);
+                    raw[4 * k] = v.x;
+                    raw[4 * k + 1] = v.y;
+                    raw[4 * k + 2] = v.z;
+                    raw[4 * k + 3] = v.w;
+                }
+                static_for<0, 16>([&](auto pp) {
+                    constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
+                    constexpr int e1 = place_of<B>(2 * decltype(pp)::value + 1);
+                    out[decltype(pp)::value] =
+                        __byte_perm(raw[e0 / 2], raw[e1 / 2],
+                                    (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
+                });
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts128(qbase + chunk_at(128, row, ql.group, k),
+                           make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(qfull);
+
+            // ---- rows of this thread: 16 hf + 8 u + g of the warp's 32
+            int lo[4], hi[4];
+            int max_lo = 0, min_hi = 0x7fffffff;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = min(row0 + set * 128 + 32 * quarter + 8 * k + g, nr - 1);
+                const int p = s.first + r / a.group;
+                hi[k] = a.causal ? p + 1 : 0x7fffffff;
+                lo[k] = a.window > 0 ? p - a.window + 1 : 0;
+                max_lo = max(max_lo, lo[k]);
+                min_hi = min(min_hi, hi[k]);
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
+                min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
+            }
+            float m[4];
+            float2 l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = -CUDART_INF_F;
+                l[k] = make_float2(0.f, 0.f);
+            }
+            const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+            const uint32_t o_t = tmem + lanes + T::kOCol + (NQ == 2 ? set * D : 0);
+            bool ok = true;
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j) {
+                const int sb = NQ == 2 ? set : (j & 1);
+                const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
+                const uint32_t s_t = tmem + lanes + sb * KT;
+                const uint32_t sc = sc_s + (j % kScaleStages) * T::kScale;
+                ok = wait.all(scfull(j % kScaleStages), (j / kScaleStages) & 1) && wait.all(sfull(sb), par);
+                if (!ok) break;
+                tmem_fence_after();
+                float x[2][KT / 2];
+                if constexpr (KT == 128) {
+                    tmem_ld_16x256b_x16(s_t, x[0]);
+                    tmem_ld_16x256b_x16(s_t + (16u << 16), x[1]);
+                } else {
+                    tmem_ld_16x256b_x8(s_t, x[0]);
+                    tmem_ld_16x256b_x8(s_t + (16u << 16), x[1]);
+                }
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
+                // ---- exponents
+                const int key0 = sp.begin + j * KT;
+                const bool masked = key0 < max_lo || key0 + KT > min_hi;
+                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                for (int k = 0; k < KT / 8; ++k) {
+                    const uint4 f = lds128(sc + (4 * k + t) * 16);
+                    const float2 ck = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+                    const float2 lv = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float* v = &x[r >> 1][4 * k + 2 * (r & 1)];
+                        const float2 y = __ffma2_rn(make_float2(v[0], v[1]), ck, lv);
+                        v[0] = y.x;
+                        v[1] = y.y;
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < KT / 8; ++k)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = key0 + 8 * k + 2 * t + e;
+                                if (key < lo[r] || key >= hi[r])
+                                    x[r >> 1][4 * k + 2 * (r & 1) + e] = -CUDART_INF_F;
+                            }
+                }
+#pragma unroll
+                for (int k = 0; k < KT / 8; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        mx[r] = fmaxf(mx[r], fmaxf(x[r >> 1][4 * k + 2 * (r & 1)],
+                                                   x[r >> 1][4 * k + 2 * (r & 1) + 1]));
+                bool far = false;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    // a row that has seen nothing: its sums are zero, any reference will do
+                    if (m[r] == -CUDART_INF_F) m[r] = mx[r];
+                    far |= mx[r] > m[r] + kLazy;
+                }
+                if (__any_sync(0xffffffffu, far)) {
+                    float f[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float nm = fmaxf(m[r], mx[r]);
+                        f[r] = nm == m[r] ? 1.f : ex2(m[r] - nm);
+                        m[r] = nm;
+                        l[r] = __fmul2_rn(l[r], make_float2(f[r], f[r]));
+                    }
+                    if (j > 0) {  // the accumulator, once the product before has landed
+                        ok = wait.all(ofull(NQ == 2 ? set : 0), (j - 1) & 1);
+                        if (!ok) break;
+                        tmem_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t at = o_t + ((uint32_t)(16 * hf) << 16) + 32 * cc;
+                                float o[16];
+                                tmem_ld_16x256b_x4(at, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[4 * k + e] *= f[2 * hf + e / 2];
+                                tmem_st_16x256b_x4(at, o);
+                            }
+                    }
+                }
+                // ---- weights
+                float2 base2[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float z = m[r] == -CUDART_INF_F ? 0.f : kShift - m[r];
+                    base2[r] = make_float2(z, z);
+                }
+                uint32_t p[2][KT / 4];
+#pragma unroll
+                for (int k = 0; k < KT / 8; ++k) {
+                    float2 rs;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(rs.x), "=f"(rs.y)
+                                 : "r"(sc + KT * 8 + (4 * k + t) * 8)
+                                 : "memory");
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float* v = &x[r >> 1][4 * k + 2 * (r & 1)];
+                        const float2 y = __fadd2_rn(make_float2(v[0], v[1]), base2[r]);
+                        const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                        l[r] = __ffma2_rn(w, rs, l[r]);
+                        p[r >> 1][2 * k + (r & 1)] = f2_to_f16x2(w.x, w.y);
+                    }
+                }
+                if constexpr (KT == 128) {
+                    tmem_st_16x128b_x16(s_t, p[0]);
+                    tmem_st_16x128b_x16(s_t + (16u << 16), p[1]);
+                } else {
+                    tmem_st_16x128b_x8(s_t, p[0]);
+                    tmem_st_16x128b_x8(s_t + (16u << 16), p[1]);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_one(pfull(sb));
+                    mbar_arrive_one(scempty(j % kScaleStages));
+                }
+            }
+            // ---- the accumulator out, 32 columns at a time through this warp's own
+            // part of the queries' tile (its rows' queries are used up: the last
+            // product has landed)
+            // (With one row set the last two products may both be outstanding -- the
+            // last scores were issued before the one but last product -- and a
+            // parity tells only neighbouring phases apart: wait for each.)
+            if (NQ == 1 && tiles > 1) ok = ok && wait.all(ofull(0), (tiles - 2) & 1);
+            if (ok && tiles > 0) ok = wait.all(ofull(NQ == 2 ? set : 0), (tiles - 1) & 1);
+            if (ok) {
+                tmem_fence_after();
+                float* stage = reinterpret_cast<float*>(base + (qbase - base_s)) + quarter * 1024;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float z = l[r].x + l[r].y;
+                    z += __shfl_xor_sync(0xffffffffu, z, 1);
+                    z += __shfl_xor_sync(0xffffffffu, z, 2);
+                    l[r].x = z;
+                }
+                const int myrow0 = row0 + set * 128 + 32 * quarter;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float o[16];
+                        if (tiles > 0) {
+                            tmem_ld_16x256b_x4(o_t + ((uint32_t)(16 * hf) << 16) + 32 * cc, o);
+                            tmem_wait_ld(o);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int rr = 16 * hf + 8 * u + g;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    // column 8k + 2t + e holds this value of the 32
+                                    const int n = 8 * k + 2 * t + e;
+                                    const int d = place_of<B>(n);
+                                    stage[rr * 32 + (d ^ ((rr & 7) * 4))] = o[4 * k + 2 * u + e];
+                                }
+                        }
+                    }
+                    __syncwarp();
+                    static_for<0, 4>([&](auto kk) {
+                        constexpr int k = decltype(kk)::value;
+                        // rows 8k .. 8k + 7, whose sums are row k's of lanes 0, 4, ..
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int rr = 8 * k + 4 * i + (lane >> 3), d = (lane & 7) * 4;
+                            const float L = __shfl_sync(0xffffffffu, l[k].x, (4 * i + (lane >> 3)) * 4);
+                            const float M = __shfl_sync(0xffffffffu, m[k], (4 * i + (lane >> 3)) * 4);
+                            const float4 y = *reinterpret_cast<const float4*>(
+                                stage + rr * 32 + (d ^ ((rr & 7) * 4)));
+                            const int row = myrow0 + rr;
+                            if (row < nr) {
+                                if (sp.count <= 1) {
+                                    k12::store_row<4>(a, s, h, row, 32 * cc + d, &y.x, M - kShift,
+                                                      L);
+                                } else {
+                                    float* dst =
+                                        part + k12::part_index(pl, c, b, h, split, row) * (D + 4);
+                                    *reinterpret_cast<float4*>(dst + 32 * cc + d) = y;
+                                    if (cc == 0 && d == 0)
+                                        *reinterpret_cast<float2*>(dst + D) =
+                                            make_float2(M - kShift, L);
+                                }
+                            }
+                        }
+                    });
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        reg_dealloc<72>();
+        if (warp == kMmaWarp) {
+            // ================= MMA issue
+            if (lane == 0 && tiles > 0) {
+                constexpr uint32_t kIdQk = idesc(true, false, KT), kIdPv = idesc(false, true, D);
+                constexpr uint32_t kPanel = KT * 128;
+                auto qk = [&](int set, int sb, int stage) {
+                    const uint32_t qa = q_s + set * 128 * T::kPanels * 128;
+                    const uint32_t ka = k_s + stage * T::kStage;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + sb * KT, desc_k(qa + (k / 4) * 128 * 128) + 2 * (k % 4),
+                               desc_k(ka + (k / 4) * kPanel) + 2 * (k % 4), kIdQk, k != 0);
+                };
+                auto pv = [&](int set, int sb, int stage, bool first) {
+                    const uint32_t va = v_s + stage * T::kStage;
+#pragma unroll
+                    for (int k = 0; k < KT / 16; ++k)
+                        mma_ts(tmem + T::kOCol + set * D, tmem + sb * KT + 8 * k,
+                               desc_v(va + k * 2048, kPanel), kIdPv, !(first && k == 0));
+                };
+                bool ok = wait.one(qfull, 0) && wait.one(kfull(0), 0);
+                tmem_fence_after();
+                if constexpr (NQ == 2) {
+                    if (ok) {
+                        for (int set = 0; set < sets; ++set) {
+                            qk(set, set, 0);
+                            commit(sfull(set));
+                        }
+                        commit(kempty(0));
+                    }
+                    for (int j = 0; j < tiles && ok; ++j) {
+                        const int st = j & 1, nx = st ^ 1;
+                        const uint32_t par = (j >> 1) & 1, npar = ((j + 1) >> 1) & 1;
+                        ok = wait.one(vfull(st), par);
+                        for (int set = 0; set < sets && ok; ++set) {
+                            ok = wait.one(pfull(set), j & 1);
+                            if (!ok) break;
+                            tmem_fence_after();
+                            pv(set, set, st, j == 0);
+                            commit(ofull(set));
+                            if (j + 1 < tiles) {
+                                if (set == 0) ok = wait.one(kfull(nx), npar);
+                                if (!ok) break;
+                                tmem_fence_after();
+                                qk(set, set, nx);
+                                commit(sfull(set));
+                            }
+                        }
+                        if (ok) {
+                            commit(vempty(st));
+                            if (j + 1 < tiles) commit(kempty(nx));
+                        }
+                    }
+                } else {
+                    if (ok) {
+                        qk(0, 0, 0);
+                        commit(sfull(0));
+                        commit(kempty(0));
+                    }
+                    for (int j = 0; j < tiles && ok; ++j) {
+                        const int st = j & 1, nx = st ^ 1;
+                        const uint32_t par = (j >> 1) & 1, npar = ((j + 1) >> 1) & 1;
+                        if (j + 1 < tiles) {
+                            // its score buffer held the weights of tile j - 1, whose
+                            // product was issued before
+                            ok = wait.one(kfull(nx), npar);
+                            if (!ok) break;
+                            tmem_fence_after();
+                            qk(0, nx, nx);
+                            commit(sfull(nx));
+                            commit(kempty(nx));
+                        }
+                        ok = wait.one(vfull(st), par) && wait.one(pfull(st), par);
+                        if (!ok) break;
+                        tmem_fence_after();
+                        pv(0, st, st, j == 0);
+                        commit(ofull(0));
+                        commit(vempty(st));
+                    }
+                }
+                // every MMA issued has completed once this commit arrives
+                commit(drain);
+                if (!mbar_wait_bounded<true>(drain, 0, kTimeoutNs))
+                    report_status(status, HBL_ERR_TIMEOUT);
+            }
+        } else if (tiles > 0) {
+            // ================= widening
+            const int cw = warp - kConvWarp0;
+            const Lane<D> ln(lane);
+            uint32_t raw[T::kMine][B];
+            // this warp's i-th unit of a tile of K (values: V's are dealt out from
+            // another warp on, so that all get about the same)
+            auto unit = [&](bool val, int i) { return (val ? (cw + 5) % kConv : cw) + kConv * i; };
+            auto load = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
+                const int u = unit(phase & 1, i);
+                const int key = sp.begin + (phase >> 1) * KT + u * Lane<D>::kRows + ln.row;
+                int page = -1;
+                if (u < T::kUnits && key < sp.end)
+                    page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
+                if (page >= 0) {
+                    const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
+                                        (key - (int)pl.div_page(key) * c.page_size);
+                    const uint8_t* src = ((phase & 1) ? c.vc : c.kc) + row * ROW_BYTES +
+                                         ln.group * (4 * B);
+                    if constexpr (B % 4 == 0) {
+#pragma unroll
+                        for (int k = 0; k < B / 4; ++k) {
+                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
+                            raw[i][4 * k] = v.x;
+                            raw[i][4 * k + 1] = v.y;
+                            raw[i][4 * k + 2] = v.z;
+                            raw[i][4 * k + 3] = v.w;
+                        }
+                    } else if constexpr (B == 2) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+                        raw[i][0] = v.x;
+                        raw[i][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < B; ++k)
+                            raw[i][k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+                    }
+                } else {  // nothing there: any finite codes (their weight is zero)
+#pragma unroll
+                    for (int k = 0; k < B; ++k) raw[i][k] = 0;
+                }
+            };
+            auto store = [&](auto bf16, int i, int u, uint32_t dst) {
+                uint32_t out[16];
+                widen32<B, decltype(bf16)::value>(raw[i], out);
+                const int row = u * Lane<D>::kRows + ln.row;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts128(dst + chunk_at(KT, row, ln.group, k),
+                           make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
+            };
+            const float xscale = a.scale * 1.4426950408889634f;
+            // scales of a tile: four positions a lane, by the last widening warp
+            float4 sk, sv;
+            bool sc_there = false;
+            auto load_scales = [&](int j) {
+                const int key = sp.begin + j * KT + 4 * lane;
+                sc_there = false;
+                if (4 * lane < KT && key < sp.end) {
+                    const int page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
+                    if (page >= 0) {
+                        const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
+                                            (key - (int)pl.div_page(key) * c.page_size);
+                        sk = *reinterpret_cast<const float4*>(c.ks + row);
+                        sv = *reinterpret_cast<const float4*>(c.vs + row);
+                        sc_there = true;
+                    } else {
+                        report_status(status, HBL_ERR_INVALID_ARG);
+                    }
+                }
+            };
+            auto store_scales = [&](int j) {
+                if (4 * lane >= KT) return;
+                const uint32_t sc = sc_s + (j % kScaleStages) * T::kScale;
+                const int key = sp.begin + j * KT + 4 * lane;
+                const float k4[4] = {sk.x, sk.y, sk.z, sk.w}, v4[4] = {sv.x, sv.y, sv.z, sv.w};
+                float ck[4], lv[4], rs[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a position that is not there: 0 * x - inf
+                    const bool there = sc_there && key + e < sp.end;
+                    ck[e] = there ? __fmul_rn(k4[e], xscale) : 0.f;
+                    // a zero scale (an all-zero row: its codes are zero too) as 2^-100
+                    lv[e] = there ? fmaxf(lg2(v4[e]), -100.f) : -CUDART_INF_F;
+                    rs[e] = there ? ex2(-lv[e]) : 0.f;
+                }
+                auto f = [](float v) { return __float_as_uint(v); };
+                sts128(sc + lane * 32, make_uint4(f(ck[0]), f(ck[1]), f(lv[0]), f(lv[1])));
+                sts128(sc + lane * 32 + 16, make_uint4(f(ck[2]), f(ck[3]), f(lv[2]), f(lv[3])));
+                sts128(sc + KT * 8 + lane * 16, make_uint4(f(rs[0]), f(rs[1]), f(rs[2]), f(rs[3])));
+            };
+            const bool scales = cw == kConv - 1;
+            if (scales) load_scales(0);
+#pragma unroll
+            for (int i = 0; i < T::kMine; ++i) load(0, i);
+            bool ok = true;
+#pragma unroll 1
+            for (int j = 0; j < tiles && ok; ++j) {
+                const int st = j & 1;
+                const uint32_t par = ((j >> 1) & 1) ^ 1;
+                if (scales) {
+                    if (j >= kScaleStages)
+                        ok = wait.all(scempty(j % kScaleStages), ((j / kScaleStages) & 1) ^ 1);
+                    if (!ok) break;
+                    store_scales(j);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(scfull(j % kScaleStages));
+                    if (j + 1 < tiles) load_scales(j + 1);
+                }
+                if (j >= 2) ok = wait.all(kempty(st), par);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < T::kMine; ++i) {
+                    const int u = unit(false, i);
+                    if (u < T::kUnits) store(ic_bool<true>{}, i, u, k_s + st * T::kStage);
+                    load(2 * j + 1, i);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(kfull(st));
+                if (j >= 2) ok = wait.all(vempty(st), par);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < T::kMine; ++i) {
+                    const int u = unit(true, i);
+                    if (u < T::kUnits) store(ic_bool<false>{}, i, u, v_s + st * T::kStage);
+                    if (j + 1 < tiles) load(2 * j + 2, i);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(vfull(st));
+            }
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+                     : "memory");
+    }
+}
+
+template <int D, int B>
+hbl_status launch(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Plan& pl, float* part,
+                  int32_t* status, cudaStream_t stream) {
+    auto kern = chunk_kernel<D, B>;
+    if (!smem_attr_once(reinterpret_cast<const void*>(kern), Tile<D>::kSmem)) return HBL_ERR_CUDA;
+    const dim3 grid((unsigned)(kb.num_seqs * pl.row_blocks * pl.splits), (unsigned)c.heads);
+    kern<<<grid, kThreads, Tile<D>::kSmem, stream>>>(c, kb, a, pl, part, status);
+    return cudaGetLastError() == cudaSuccess ? HBL_OK : HBL_ERR_CUDA;
+}
+
+template <int D>
+hbl_status launch_d(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Plan& pl,
+                    float* part, int32_t* status, cudaStream_t stream) {
+    switch (c.bits) {
+        case 2: return launch<D, 2>(c, kb, a, pl, part, status, stream);
+        case 3: return launch<D, 3>(c, kb, a, pl, part, status, stream);
+        case 4: return launch<D, 4>(c, kb, a, pl, part, status, stream);
+        default: return launch<D, 8>(c, kb, a, pl, part, status, stream);
+    }
+}
+
+}  // namespace k14
+}  // namespace hbl
