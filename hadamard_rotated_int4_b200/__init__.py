@@ -25,6 +25,7 @@ Names follow include/hbl.h:
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libhbl.so")
@@ -51,6 +52,7 @@ EXPORTS = ("hbl_status_string", "hbl_version", "hbl_workspace_size", "hbl_worksp
            "hbl_probe_tc_int8")
 
 _lib = None
+_kv_calls = {}  # the KV calls once more, taking packed bytes for their structs
 
 
 class _CacheArgs(ctypes.Structure):  # hbl_kv_cache
@@ -135,6 +137,12 @@ def lib():
         L.hbl_kv_attention_workspace.argtypes = [CA, BA, AA, ctypes.POINTER(SZ)]
         L.hbl_kv_attention.restype = I
         L.hbl_kv_attention.argtypes = [CA, BA, AA, P, SZ, P, P]
+        for name in ("hbl_kv_cache_write", "hbl_kv_cache_read", "hbl_kv_attention_workspace",
+                     "hbl_kv_attention"):
+            f = L[name]
+            f.restype = I
+            f.argtypes = [P if t in (CA, BA, AA) else t for t in getattr(L, name).argtypes]
+            _kv_calls[name] = f
         L.hbl_expand_ternary.restype = I
         L.hbl_expand_ternary.argtypes = [P, I, I, P, P, P]
         L.hbl_ternary_gemm_s8w.restype = I
@@ -406,38 +414,47 @@ def kv_quant(X, bits, eps=1e-5, out=None, status=None):
 
 
 # ------------------------------------------------------- paged low-bit KV cache
+# These calls run once per layer and token, so their marshalling is kept short:
+# the structs are packed bytes, and the stream is asked for by device index.
+
+_pack_cache = struct.Struct("@PPPPiiiii4x").pack         # hbl_kv_cache
+_pack_batch = struct.Struct("@PPPiii4x").pack           # hbl_kv_batch
+_pack_attn = struct.Struct("@PqqPqqPiiifii").pack       # hbl_kv_attn
+
 
 class KvCache:
     """A paged low-bit K/V cache: uint8 codes [pages, heads, page_size, D*bits/8]
     and fp32 scales [pages, heads, page_size], for K and for V (hbl_kv_cache)."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "num_pages", "num_kv_heads",
-                 "page_size", "head_dim", "bits", "device", "_args")
+                 "page_size", "head_dim", "bits", "device", "_index", "_args")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim):
         import torch
 
-        for t, dt, name in ((k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
-                            (k_scales, torch.float32, "k_scales"),
-                            (v_scales, torch.float32, "v_scales")):
-            _dev(t, dt, name)
-        shape = k_scales.shape
-        if len(shape) != 3 or k_codes.dim() != 4 or k_codes.shape[:3] != shape or \
-                v_codes.shape != k_codes.shape or v_scales.shape != shape:
+        _dev(k_codes, torch.uint8, "k_codes")
+        _dev(v_codes, torch.uint8, "v_codes")
+        _dev(k_scales, torch.float32, "k_scales")
+        _dev(v_scales, torch.float32, "v_scales")
+        shape, code_shape = k_scales.shape, k_codes.shape
+        if len(shape) != 3 or len(code_shape) != 4 or code_shape[:3] != shape or \
+                v_codes.shape != code_shape or v_scales.shape != shape:
             raise ValueError("codes must be [pages, heads, page_size, D*bits/8] and scales "
                              "[pages, heads, page_size], alike for K and V")
-        if not k_codes.device == v_codes.device == k_scales.device == v_scales.device:
+        self.device = device = k_codes.device
+        if not device == v_codes.device == k_scales.device == v_scales.device:
             raise ValueError("the cache's tensors must be on one device")
         self.num_pages, self.num_kv_heads, self.page_size = shape
-        self.head_dim, self.device = int(head_dim), k_codes.device
-        self.bits = k_codes.shape[3] * 8 // self.head_dim if self.head_dim > 0 else 0
-        if self.head_dim < 1 or kv_code_bytes(self.head_dim, self.bits) != k_codes.shape[3]:
+        self.head_dim = head_dim = int(head_dim)
+        self._index = device.index
+        nbytes = code_shape[3]
+        self.bits = bits = nbytes * 8 // head_dim if head_dim > 0 else 0
+        if head_dim < 1 or kv_code_bytes(head_dim, bits) != nbytes:
             raise ValueError("the codes' last dimension must be head_dim * bits / 8 bytes")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
                                                                    v_scales)
-        self._args = _CacheArgs(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                v_scales.data_ptr(), self.num_pages, self.page_size,
-                                self.num_kv_heads, self.head_dim, self.bits)
+        self._args = _pack_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                 v_scales.data_ptr(), shape[0], shape[2], shape[1], head_dim, bits)
 
 
 def kv_cache_alloc(num_pages, page_size, num_kv_heads, head_dim, bits, device):
@@ -455,19 +472,18 @@ def _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows):
     """hbl_kv_batch of int32 CUDA tensors on the cache's device."""
     import torch
 
-    for t, name, dims in ((cu_seqlens, "cu_seqlens", 1), (kv_lens, "kv_lens", 1),
-                          (block_table, "block_table", 2)):
-        _dev(t, torch.int32, name)
-        if t.dim() != dims:
-            raise ValueError("%s must have %d dimension(s)" % (name, dims))
-        if t.device != cache.device:
-            raise ValueError("%s must be on the cache's device" % name)
-    n = kv_lens.shape[0]
-    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
-        raise ValueError("cu_seqlens must have one entry more, block_table as many rows as "
-                         "kv_lens has entries")
-    return _BatchArgs(cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n,
-                      block_table.shape[1], int(rows))
+    i32 = torch.int32
+    _dev(cu_seqlens, i32, "cu_seqlens")
+    _dev(kv_lens, i32, "kv_lens")
+    _dev(block_table, i32, "block_table")
+    if not cu_seqlens.device == kv_lens.device == block_table.device == cache.device:
+        raise ValueError("cu_seqlens, kv_lens and block_table must be on the cache's device")
+    n, cu, table = kv_lens.shape, cu_seqlens.shape, block_table.shape
+    if len(n) != 1 or len(cu) != 1 or len(table) != 2 or cu[0] != n[0] + 1 or table[0] != n[0]:
+        raise ValueError("kv_lens must be [seqs], cu_seqlens [seqs + 1] and block_table "
+                         "[seqs, pages]")
+    return _pack_batch(cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n[0],
+                       table[1], rows)
 
 
 def _kv_rows(t, cache, name, heads=None):
@@ -480,43 +496,41 @@ def _kv_rows(t, cache, name, heads=None):
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if t.device != cache.device:
         raise ValueError("%s must be on the cache's device" % name)
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or \
-            (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
         raise ValueError("%s must be [rows, heads, head_dim] like the cache" % name)
     sr, sh, sd = t.stride()
     if sd != 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
     # the stride of a dimension of one is never used
-    return sr if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0
+    return sr if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
 
 
-def _on(device):
-    """The device's current stream, and the device made current for the call."""
+def _kv_call(what, cache, *args):
+    """Calls the library on the cache's device and that device's current stream."""
     import torch
 
-    index = device.index
-    guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-    return guard, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _kv_call(what, device, *args):
-    guard, stream = _on(device)
-    if guard is None:
-        status = getattr(lib(), what)(*args, stream)
+    lib()
+    index = cache._index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        status = _kv_calls[what](*args, stream)
     else:
-        with guard:
-            status = getattr(lib(), what)(*args, stream)
-    _check(status, what)
+        with torch.cuda.device(index):
+            status = _kv_calls[what](*args, stream)
+    if status != HBL_OK:
+        raise HblError(status, what)
 
 
 def _kv_status(status, cache):
     import torch
 
-    if status is not None:
-        _dev(status, torch.int32, "status")
-        if status.device != cache.device:
-            raise ValueError("status must be on the cache's device")
-    return _ptr(status)
+    if status is None:
+        return None
+    _dev(status, torch.int32, "status")
+    if status.device != cache.device:
+        raise ValueError("status must be on the cache's device")
+    return status.data_ptr()
 
 
 def kv_cache_write(cache, K, V, cu_seqlens, kv_lens, block_table, eps=1e-5, status=None):
@@ -524,10 +538,11 @@ def kv_cache_write(cache, K, V, cu_seqlens, kv_lens, block_table, eps=1e-5, stat
     row and head strides that are multiples of 8) into the batch's pages."""
     ks = _kv_rows(K, cache, "K", cache.num_kv_heads)
     vs = _kv_rows(V, cache, "V", cache.num_kv_heads)
-    if K.shape != V.shape:
+    rows = K.shape[0]
+    if V.shape[0] != rows:
         raise ValueError("K and V must have the same shape")
-    batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, K.shape[0])
-    _kv_call("hbl_kv_cache_write", cache.device, cache._args, batch, K.data_ptr(), ks[0], ks[1],
+    batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
+    _kv_call("hbl_kv_cache_write", cache, cache._args, batch, K.data_ptr(), ks[0], ks[1],
              V.data_ptr(), vs[0], vs[1], float(eps), _kv_status(status, cache))
 
 
@@ -537,13 +552,16 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
     sequence as (K, V) [rows, heads, D], bf16 (default) or torch.float32."""
     import torch
 
-    shape = (int(rows), cache.num_kv_heads, cache.head_dim)
+    rows = int(rows)
+    shape = (rows, cache.num_kv_heads, cache.head_dim)
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("dtype must be torch.bfloat16 or torch.float32, got %s" % dtype)
+        if rows < 0:
+            raise ValueError("rows must not be negative")
         K = torch.empty(shape, dtype=dtype, device=cache.device)
-        V = torch.empty(shape, dtype=dtype, device=cache.device)
+        V = torch.empty_like(K)
     else:
         K, V = out
         dtype = K.dtype if dtype is None else dtype
@@ -554,21 +572,26 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
             if tuple(t.shape) != shape or t.device != cache.device:
                 raise ValueError("out must be two [rows, heads, D] tensors on the cache's device")
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
-    _kv_call("hbl_kv_cache_read", cache.device, cache._args, batch, K.data_ptr(), V.data_ptr(),
+    _kv_call("hbl_kv_cache_read", cache, cache._args, batch, K.data_ptr(), V.data_ptr(),
              1 if dtype == torch.float32 else 0, _kv_status(status, cache))
     return K, V
+
+
+def _kv_attention_bytes(cache_args, batch, args):
+    lib()
+    need = ctypes.c_size_t(0)
+    _check(_kv_calls["hbl_kv_attention_workspace"](cache_args, batch, args, ctypes.byref(need)),
+           "hbl_kv_attention_workspace")
+    return need.value
 
 
 def kv_attention_workspace_size(rows, num_heads, cache, num_seqs, pages_per_seq, max_rows=0,
                                 max_kv=0, causal=True, window=0):
     """Workspace bytes of kv_attention for these sizes."""
-    batch = _BatchArgs(None, None, None, int(num_seqs), int(pages_per_seq), int(rows))
-    args = _AttnArgs(None, 0, 0, None, 0, 0, None, int(num_heads), int(max_rows or 0),
-                     int(max_kv or 0), 1.0, int(bool(causal)), int(window))
-    need = ctypes.c_size_t(0)
-    _check(lib().hbl_kv_attention_workspace(cache._args, batch, args, ctypes.byref(need)),
-           "hbl_kv_attention_workspace")
-    return need.value
+    batch = _pack_batch(0, 0, 0, int(num_seqs), int(pages_per_seq), int(rows))
+    args = _pack_attn(0, 0, 0, 0, 0, 0, 0, int(num_heads), int(max_rows or 0), int(max_kv or 0),
+                      1.0, 1 if causal else 0, int(window))
+    return _kv_attention_bytes(cache._args, batch, args)
 
 
 def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_kv=None,
@@ -582,31 +605,31 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     Returns O (out if given), with want_lse also lse fp32 [rows, q heads]."""
     import torch
 
-    qs = _kv_rows(Q, cache, "Q")
+    q_row, q_head = _kv_rows(Q, cache, "Q")
     rows, heads, D = Q.shape
-    O = torch.empty((rows, heads, D), dtype=torch.bfloat16, device=cache.device) \
-        if out is None else out
-    os_ = _kv_rows(O, cache, "out", heads)
-    if O.shape[0] != rows:
+    if out is None:
+        out = torch.empty((rows, heads, D), dtype=torch.bfloat16, device=cache.device)
+    o_row, o_head = _kv_rows(out, cache, "out", heads)
+    if out.shape[0] != rows:
         raise ValueError("out must have Q's shape")
     lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) \
         if want_lse else None
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
-    args = _AttnArgs(Q.data_ptr(), qs[0], qs[1], O.data_ptr(), os_[0], os_[1],
-                     None if lse is None else lse.data_ptr(), heads, int(max_rows or 0),
-                     int(max_kv or 0), D ** -0.5 if scale is None else float(scale),
-                     int(bool(causal)), int(window))
+    args = _pack_attn(Q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,
+                      lse.data_ptr() if want_lse else 0, heads, max_rows or 0, max_kv or 0,
+                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window)
     if ws is None:
-        need = ctypes.c_size_t(0)
-        _check(lib().hbl_kv_attention_workspace(cache._args, batch, args, ctypes.byref(need)),
-               "hbl_kv_attention_workspace")
-        if need.value:
-            ws = _workspace(need.value, cache.device)
-    elif not ws.is_cuda or ws.device != cache.device or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous tensor on the cache's device")
-    _kv_call("hbl_kv_attention", cache.device, cache._args, batch, args, _ptr(ws),
-             0 if ws is None else ws.numel() * ws.element_size(), _kv_status(status, cache))
-    return (O, lse) if want_lse else O
+        nbytes = _kv_attention_bytes(cache._args, batch, args)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    else:
+        if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != cache.device or \
+                not ws.is_contiguous():
+            raise ValueError("ws must be a contiguous tensor on the cache's device")
+        nbytes = ws.numel() * ws.element_size()
+    _kv_call("hbl_kv_attention", cache, cache._args, batch, args,
+             None if ws is None else ws.data_ptr(), nbytes, _kv_status(status, cache))
+    return (out, lse) if want_lse else out
 
 
 # ------------------------------------------------------- expanded weights

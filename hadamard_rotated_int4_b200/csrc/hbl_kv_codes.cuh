@@ -31,6 +31,18 @@ __device__ __forceinline__ uint32_t bfma2_u(uint32_t a, uint32_t b, uint32_t c) 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// (x & mask) | bits in one operation (written as two, the compiler makes two of
+// them: only one of its operands can be a constant).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
 // Bits of a small power-of-two or integer-valued constant, both halves.
 __host__ __device__ constexpr uint32_t pow2_f16(int e) { return (uint32_t)((e + 15) << 10); }
 __host__ __device__ constexpr uint32_t pow2_bf16(int e) { return (uint32_t)((e + 127) << 7); }
@@ -51,7 +63,7 @@ __device__ __forceinline__ void kv_widen_f16(uint32_t x, uint32_t (&out)[N]) {
     static_for<0, N>([&](auto ii) {
         constexpr int i = decltype(ii)::value, at = B * (i % kPer), sh = B * (i - i % kPer);
         constexpr uint32_t mask = twice(((1u << B) - 1u) << at);
-        const uint32_t v = ((x >> sh) & mask) | 0x64006400u;  // 1024 + u * 2^at
+        const uint32_t v = and_or(x >> sh, mask, 0x64006400u);  // 1024 + u * 2^at
         out[i] = hfma2_u(v, twice(pow2_f16(-at)), twice(neg_int_bits((1024 >> at) + kOff, 10, 15)));
     });
 }
@@ -66,12 +78,12 @@ __device__ __forceinline__ void kv_widen_bf16(uint32_t x, uint32_t (&out)[N]) {
             // 128 + (u & 127), then -256, or -128 where u's top bit is set (the
             // two constants differ in that bit): u - 128 either way
             const uint32_t y = x >> (8 * i);
-            out[i] = bfma2_u((y & 0x007f007fu) | 0x43004300u, twice(pow2_bf16(0)),
-                             (y & 0x00800080u) ^ 0xC380C380u);
+            out[i] = bfma2_u(and_or(y, 0x007f007fu, 0x43004300u), twice(pow2_bf16(0)),
+                             and_xor(y, 0x00800080u, 0xC380C380u));
         } else {
             constexpr int at = B * (i % kPer), sh = B * (i - i % kPer);
             constexpr uint32_t mask = twice(((1u << B) - 1u) << at);
-            const uint32_t v = ((x >> sh) & mask) | 0x43004300u;  // 128 + u * 2^at
+            const uint32_t v = and_or(x >> sh, mask, 0x43004300u);  // 128 + u * 2^at
             out[i] = bfma2_u(v, twice(pow2_bf16(-at)),
                              twice(neg_int_bits((128 >> at) + kOff, 7, 127)));
         }
@@ -83,9 +95,10 @@ __device__ __forceinline__ void kv_widen_bf16(uint32_t x, uint32_t (&out)[N]) {
 template <int B, int N>
 constexpr int kKvWords = (N + 2 * kKvHalfCodes<B> - 1) / (2 * kKvHalfCodes<B>);
 
-// 24 bits of eight 3-bit codes -> two 12-bit halves.
+// 24 bits of eight 3-bit codes -> two 12-bit halves (what lies above them in
+// either half is not cleared: every code is masked out by itself).
 __device__ __forceinline__ uint32_t kv_spread3(uint32_t c) {
-    return (c & 0xfffu) | ((c << 4) & 0x0fff0000u);
+    return __byte_perm(c, c << 4, 0x7610);
 }
 
 template <int B, int N>

@@ -5,56 +5,104 @@
 namespace hbl {
 namespace k12 {
 
-// Joins the ranges of a head row: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// One warp per head row, D/32 values a lane; a row with one range was stored by
-// the kernel that computed it.
+// Joins `count` parts of a head row: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s;
+// D/4 threads (four values each) to a part, 4 * kThreads / D parts at once, four
+// loads of each thread in flight.  Part 0 lies at src0, part k > 0 at src + k * next.
 constexpr int kThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) combine_kernel(KvCache c, KvBatch kb, KvAttn a, Plan pl,
-                                                           const float* part) {
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int rows = pl.row_blocks * pl.block_rows;
-    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int row = (int)(w % rows), h = (int)(w / rows % c.heads), b = (int)(w / rows / c.heads);
-    Rows s = {};
-    int count = 0;
-    if (b < kb.num_seqs) {
-        s = rows_of(kb, c.page_size, a, b);
-        const int nr = s.n * a.group, r0 = row / pl.block_rows * pl.block_rows;
-        if (row < nr && nr >= pl.min_rows && nr <= pl.max_rows)
-            count = split_of(pl, range_of(a, s, r0, min(nr, r0 + pl.block_rows) - 1), 0).count;
+__device__ __forceinline__ void join_row(const KvAttn& a, const Rows& s, int h, int row, int count,
+                                         const float* src0, const float* src, int64_t next) {
+    constexpr int T = D / 4, G = kThreads / T;  // threads of a part, parts at once
+    constexpr int U = 4;
+    __shared__ float4 sy[kThreads];
+    __shared__ float sl[G];
+    const int t = threadIdx.x % T, g = threadIdx.x / T;
+    auto part_of = [&](int k) { return k == 0 ? src0 : src + k * next; };
+    float M = -CUDART_INF_F;  // every warp for itself
+    for (int k = threadIdx.x & 31; k < count; k += 32) M = fmaxf(M, part_of(k)[D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = g; k < count; k += G * U) {
+        float4 v[U];
+        float2 ml[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = k + u * G < count;
+            const float* p = part_of(in ? k + u * G : k);
+            v[u] = reinterpret_cast<const float4*>(p)[t];
+            ml[u] = *reinterpret_cast<const float2*>(p + D);
+            if (!in) ml[u].x = -CUDART_INF_F;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = ml[u].x == -CUDART_INF_F ? 0.f : exp2f(ml[u].x - M);
+            L = __fmaf_rn(ml[u].y, f, L);
+            y.x = __fmaf_rn(v[u].x, f, y.x);
+            y.y = __fmaf_rn(v[u].y, f, y.y);
+            y.z = __fmaf_rn(v[u].z, f, y.z);
+            y.w = __fmaf_rn(v[u].w, f, y.w);
+        }
+    }
+    sy[threadIdx.x] = y;
+    if (t == 0) sl[g] = L;
+    __syncthreads();
+    if (g != 0) return;
+    const int most = min(count, G);
+    for (int k = 1; k < most; ++k) {
+        const float4 z = sy[k * T + t];
+        L += sl[k];
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+    }
+    store_row<4>(a, s, h, row, 4 * t, &y.x, M, L);
+}
+
+// Few rows: CTA (i, r) joins row r of the one head of an item that begins in piece
+// i of the line and goes on past it (all others were stored by the kernel that
+// computed them).
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_pieces_kernel(KvCache c, KvBatch kb, KvAttn a,
+                                                               Plan pl, float* part) {
+    const Line line = line_of<kThreads, true>(pl, c, kb, a, blockIdx.x, nullptr);
+    Item im = {};
+    int h = 0, count = 0, row = 0;
+    if (line.at < line.total) {
+        im = item_of(pl, c, kb, a, line.item);
+        h = (line.at - line.before) / im.units;
+        const int first = line.before + h * im.units, last = first + im.units - 1;
+        row = line.item % pl.row_blocks * pl.block_rows + (int)blockIdx.y;
+        if (first >= (int)blockIdx.x * line.per && last > line.at && row < im.nr)
+            count = last / line.per - (int)blockIdx.x + 1;
     }
     // every thread waits: the grid must not end before the one it depends on
     pdl_wait();
+    if (count > 1)
+        join_row<D>(a, im.s, h, row, count,
+                    slot_of(part, pl, D, blockIdx.x, 1) + blockIdx.y * (D + 4),
+                    slot_of(part, pl, D, blockIdx.x, 0) + blockIdx.y * (D + 4),
+                    2 * pl.block_rows * (D + 4));
+}
+
+// Chunks: one CTA to a head row, whose ranges of positions it joins.
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_ranges_kernel(KvCache c, KvBatch kb, KvAttn a,
+                                                               Plan pl, const float* part) {
+    const int rows = pl.row_blocks * pl.block_rows, bh = (int)(blockIdx.x / rows);
+    const int row = (int)(blockIdx.x - (int64_t)bh * rows), b = bh / c.heads, h = bh - b * c.heads;
+    const Rows s = rows_of(kb, c.page_size, a, b);
+    const int nr = s.n * a.group, r0 = row / pl.block_rows * pl.block_rows;
+    int count = 0;
+    if (row < nr && nr >= pl.min_rows && nr <= pl.max_rows)
+        count = split_of(pl, range_of(a, s, r0, min(nr, r0 + pl.block_rows) - 1), 0).count;
+    pdl_wait();
     if (count <= 1) return;
     const float* src = part + part_index(pl, c, b, h, 0, row) * (D + 4);
-    const int64_t next = (int64_t)rows * (D + 4);
-    float M = -CUDART_INF_F;
-    for (int k = lane; k < count; k += 32) M = fmaxf(M, src[k * next + D]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = 0.f;
-    for (int k = 0; k < count; ++k) {
-        const float* p = src + k * next;
-        const float m = p[D], f = m == -CUDART_INF_F ? 0.f : exp2f(m - M);
-        L = __fmaf_rn(p[D + 1], f, L);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = __fmaf_rn(p[32 * i + lane], f, y[i]);
-    }
-    const int i = row / a.group, head = h * a.group + (row - i * a.group);
-    const int64_t t = s.row0 + i;
-    const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
-    uint16_t* dst = a.o + t * a.o_row + (int64_t)head * a.o_head;
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        dst[32 * k + lane] = (uint16_t)(f2_to_bf16x2(y[k] * inv, 0.f) & 0xffffu);
-    if (a.lse != nullptr && lane == 0)
-        a.lse[t * a.heads + head] =
-            L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
+    join_row<D>(a, s, h, row, count, src, src, (int64_t)rows * (D + 4));
 }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -67,6 +115,7 @@ constexpr int kFewRows = 32;
 static void set_page(Plan* p, int page_size) {
     uint32_t l = 0;
     while ((1ull << l) < (uint32_t)page_size) ++l;
+    p->seg_shift = page_size % 64 == 0 ? 6 : page_size % 32 == 0 ? 5 : 4;
     p->page_shift = l;
     p->page_mul = (uint32_t)((((1ull << l) - page_size) << 32) / page_size + 1);
 }
@@ -83,17 +132,24 @@ static void set_splits(Plan* p, int64_t span, int64_t quantum) {
     p->quantum = (int)(q < 0x40000000 ? q : 0x40000000);
 }
 
-// Few rows: 8 or 16 head rows a CTA, ranges so that every SM has a few CTAs.
+// Few rows: blocks of 8 or 16 head rows; as many CTAs as run at once, so that all
+// work is one wave of equal pieces.
 static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_t rows) {
     Plan p = {};
     p.block_rows = c.D <= 128 && rows > 8 ? 16 : 8;
     p.row_blocks = (int)ceil_div(rows, p.block_rows);
     p.min_rows = 0;
     p.max_rows = (int)rows;
-    const int64_t span = span_of(a, a.max_rows);
-    const int64_t ctas = (int64_t)b.num_seqs * c.heads * p.row_blocks;
-    const int64_t q = ceil_div(ctas * span, kSizingSms * 6);
-    set_splits(&p, span, q < 256 ? 256 : q);
+    p.ctas = kSizingSms * (p.block_rows == 8 && c.D <= 128 ? 3 : 2);
+    p.min_units = 4;
+    // the whole line stays below 2^31 units
+    const int64_t longest = (int64_t)b.pages_per_seq * c.page_size;
+    const int64_t items = (int64_t)b.num_seqs * p.row_blocks * c.heads;
+    p.unit = 64;
+    while (p.unit < (1 << 30) && items * (longest / p.unit + 2) > 0x7fffffffll) p.unit *= 2;
+    // no more CTAs than the block table has room for pieces
+    const int64_t most = ceil_div(items * (longest / p.unit + 2), p.min_units);
+    if (most < p.ctas) p.ctas = (int)most;
     set_page(&p, c.page_size);
     return p;
 }
@@ -136,26 +192,41 @@ static Plans plans_of(const KvCache& c, const KvBatch& b, const KvAttn& a) {
     return p;
 }
 static size_t part_bytes(const KvCache& c, const KvBatch& b, const Plan& p) {
+    if (p.ctas > 0) return (size_t)p.ctas * 2 * p.block_rows * (c.D + 4) * sizeof(float);
     if (p.splits == 1) return 0;
     return (size_t)b.num_seqs * c.heads * p.splits * p.row_blocks * p.block_rows * (c.D + 4) *
            sizeof(float);
 }
+// Grids, and the few-rows kernel's line of units, fit 31 bits.
 static bool fits(const KvCache& c, const KvBatch& b, const Plan& p) {
-    return (int64_t)b.num_seqs * p.row_blocks * p.splits <= 0x7fffffffll &&
-           ceil_div((int64_t)b.num_seqs * c.heads * p.row_blocks * p.block_rows, 4) <= 0x7fffffffll;
+    const int64_t items = (int64_t)b.num_seqs * p.row_blocks;
+    if (items * c.heads * p.block_rows > 0x7fffffffll) return false;
+    if (p.ctas > 0)
+        return items * c.heads * ((int64_t)b.pages_per_seq * c.page_size / p.unit + 2) <=
+               0x7fffffffll;
+    return items * p.splits <= 0x7fffffffll;
 }
 
+template <int D>
+static hbl_status combine_d(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p,
+                            float* part, cudaStream_t stream) {
+    if (p.ctas > 0)
+        return launch_pdl(join_pieces_kernel<D>, 
+                          dim3((unsigned)p.ctas, (unsigned)(p.max_rows < p.block_rows ? p.max_rows : p.block_rows)),
+                          dim3(kThreads), 0, stream, c, b, a, p, part);
+    return launch_pdl(join_ranges_kernel<D>,
+                      dim3((unsigned)((int64_t)b.num_seqs * c.heads * p.row_blocks *
+                                      p.block_rows)),
+                      dim3(kThreads), 0, stream, c, b, a, p, part);
+}
 static hbl_status combine(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p,
-                          const float* part, cudaStream_t stream) {
-    if (p.splits == 1) return HBL_OK;
-    const dim3 grid((unsigned)ceil_div(
-        (int64_t)b.num_seqs * c.heads * p.row_blocks * p.block_rows, kThreads / 32)),
-        block(kThreads);
+                          float* part, cudaStream_t stream) {
+    if (p.ctas == 0 && p.splits == 1) return HBL_OK;
     switch (c.D) {
-        case 32: return launch_pdl(combine_kernel<32>, grid, block, 0, stream, c, b, a, p, part);
-        case 64: return launch_pdl(combine_kernel<64>, grid, block, 0, stream, c, b, a, p, part);
-        case 128: return launch_pdl(combine_kernel<128>, grid, block, 0, stream, c, b, a, p, part);
-        default: return launch_pdl(combine_kernel<256>, grid, block, 0, stream, c, b, a, p, part);
+        case 32: return combine_d<32>(c, b, a, p, part, stream);
+        case 64: return combine_d<64>(c, b, a, p, part, stream);
+        case 128: return combine_d<128>(c, b, a, p, part, stream);
+        default: return combine_d<256>(c, b, a, p, part, stream);
     }
 }
 

@@ -14,13 +14,17 @@
 namespace hbl {
 namespace k12 {
 
-// How the launch is split; made on the host from sizes alone (few_plan, chunk_plan).
+// How a launch is laid out; made on the host from sizes alone (few_plan,
+// chunk_plan).
 struct Plan {
-    int block_rows;  // head rows of a CTA
-    int row_blocks;  // CTAs to a sequence's head rows
+    int block_rows;          // head rows of a CTA
+    int row_blocks;          // blocks to a sequence's head rows
     int min_rows, max_rows;  // the kernel takes sequences with so many head rows
-    int splits;      // most ranges of positions of one row block
-    int quantum;     // positions of a range (more where `splits` ranges would not reach)
+    int splits;              // chunks: most ranges of positions of one row block
+    int quantum;             // chunks: positions of a range (more where `splits` do not reach)
+    int ctas, min_units;     // few rows: CTAs, and the fewest units that are worth one
+    int unit;                // few rows: positions of a unit, a multiple of 64
+    int seg_shift;           // 16, 32 or 64 positions (log2) that a page holds a multiple of
     uint32_t page_mul, page_shift;  // x / page_size = (mulhi(x, mul) + x) >> shift, x < 2^31
 
     __device__ __forceinline__ uint32_t div_page(uint32_t x) const {
@@ -58,15 +62,15 @@ __device__ __forceinline__ Range range_of(const KvAttn& a, const Rows& s, int r0
     return w;
 }
 
-// Range number `split` of a row block's positions: whole groups of 16 (a group
-// never crosses a page), equal ones, the last one shorter.
+// Range number `split` of a row block's positions: whole groups of 64 from a
+// multiple of 64 on, equal ones, the last one shorter.
 struct Split {
     int begin, end;
     int count;  // ranges of this row block
 };
 __device__ __forceinline__ Split split_of(const Plan& pl, const Range& rg, int split) {
     Split s;
-    const int from = rg.begin & ~15, total = rg.end > rg.begin ? rg.end - from : 0;
+    const int from = rg.begin & ~63, total = rg.end > rg.begin ? rg.end - from : 0;
     const int q = max(pl.quantum, ((total + pl.splits - 1) / pl.splits + 127) & ~127);
     s.count = (total + q - 1) / q;
     s.begin = from + split * q;
@@ -74,11 +78,123 @@ __device__ __forceinline__ Split split_of(const Plan& pl, const Range& rg, int s
     return s;
 }
 
-// Partial results: [seq][cached head][split][row] x (D values, m, sum, 2 unused).
+// Partial results of chunks: [seq][cached head][split][row] x (D values, m, sum, 2 unused).
 __device__ __forceinline__ int64_t part_index(const Plan& pl, const KvCache& c, int b, int h,
                                               int split, int row) {
     return (((int64_t)b * c.heads + h) * pl.splits + split) * ((int64_t)pl.row_blocks *
                                                                pl.block_rows) + row;
+}
+
+// ---- few rows: all work in one line, cut into equal pieces
+// An item is one row block of one sequence on every cached head: heads times
+// `units` units of pl.unit positions.  The line runs item by item, head by head;
+// CTA i takes units [i * per, (i + 1) * per), whichever sequences they are of.  The
+// host makes the unit large enough for the line to fit 31 bits.
+struct Item {
+    Rows s;
+    Range rg;
+    int nr, from, units;  // head rows of the sequence; first position; units of one head
+};
+__device__ __forceinline__ Item item_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
+                                        const KvAttn& a, int i) {
+    Item t;
+    const int b = i / pl.row_blocks, r0 = (i - b * pl.row_blocks) * pl.block_rows;
+    t.s = rows_of(kb, c.page_size, a, b);
+    t.nr = t.s.n * a.group;
+    t.units = 0;
+    if (t.nr >= pl.min_rows && t.nr <= pl.max_rows && r0 < t.nr) {
+        t.rg = range_of(a, t.s, r0, min(t.nr, r0 + pl.block_rows) - 1);
+        t.from = t.rg.begin & ~63;
+        // a block that sees nothing still has its rows stored
+        t.units = max(1, (int)((uint32_t)(t.rg.end - t.from + pl.unit - 1) / (uint32_t)pl.unit));
+    }
+    return t;
+}
+
+// Units of a CTA of a line of `total`.
+__device__ __forceinline__ int cut(const Plan& pl, int total) {
+    const uint32_t n = min(max((uint32_t)total / (uint32_t)pl.min_units, 1u), (uint32_t)pl.ctas);
+    return (int)(((uint32_t)total + n - 1) / n);
+}
+
+// The line's cut, and where the first unit of piece `cta` lies (LAST: its last
+// unit); by all threads.  The items' units are summed once, and once more up to
+// that unit where they are more than one to a thread.
+struct Line {
+    int total, per;
+    int at;            // that unit; not below `total`: there is no such piece
+    int item, before;  // of that unit; the line's units before the item
+};
+template <int kThreads, bool LAST>
+__device__ __forceinline__ Line line_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
+                                        const KvAttn& a, int cta, int32_t* status) {
+    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int found[2];
+    const int items = kb.num_seqs * pl.row_blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Line line;
+    int mine = 0;
+    bool bad = false;
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+        const Item t = item_of(pl, c, kb, a, i);
+        mine += t.units * c.heads;
+        bad |= t.s.bad;
+    }
+    if (bad) report_status(status, HBL_ERR_INVALID_ARG);
+    // inclusive sums over the CTA: v's up to this thread, and of all
+    auto scan = [&](int v, int* all) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) warp_sum[warp] = v;
+        __syncthreads();
+        *all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) v += warp_sum[w];
+            *all += warp_sum[w];
+        }
+        return v;
+    };
+    const int upto = scan(mine, &line.total);
+    line.per = cut(pl, line.total);
+    const int64_t first = (int64_t)cta * line.per;
+    line.at = line.total;
+    if (first >= line.total) return line;  // the same for the whole CTA
+    line.at = (int)(LAST ? min(first + line.per, (int64_t)line.total) - 1 : first);
+    const int at = line.at;
+    if (items <= kThreads) {
+        if (at >= upto - mine && at < upto) {
+            found[0] = threadIdx.x;
+            found[1] = upto - mine;
+        }
+    } else {
+        int before = 0;
+        for (int i = 0; i < items && before <= at; i += kThreads) {
+            int v = 0, all;
+            if (i + (int)threadIdx.x < items)
+                v = item_of(pl, c, kb, a, i + threadIdx.x).units * c.heads;
+            __syncthreads();  // the sums of the step before are read
+            const int u = before + scan(v, &all);
+            if (at >= u - v && at < u) {
+                found[0] = i + threadIdx.x;
+                found[1] = u - v;
+            }
+            before += all;
+        }
+    }
+    __syncthreads();
+    line.item = found[0];
+    line.before = found[1];
+    return line;
+}
+
+// Partial results of few rows: two slots to a CTA, of the piece that goes on from
+// the CTA before (0) and of one that begins here and ends elsewhere (1).
+__device__ __forceinline__ float* slot_of(float* part, const Plan& pl, int D, int64_t cta, int slot) {
+    return part + (cta * 2 + slot) * pl.block_rows * (D + 4);
 }
 
 // Values d .. d + N - 1 of a head row from its weighted sum y and sum of weights

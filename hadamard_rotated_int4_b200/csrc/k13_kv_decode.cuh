@@ -7,28 +7,34 @@
 //   O   = sum_i 2^(x_i - m) v_i / sum_i 2^(x_i - m) / sv_i,   m = max x_i
 // in one pass with the running m: taking V's scale into the exponent leaves the
 // integer codes as the second product's operand, and the weights 2^(x_i - m)
-// in (0, 1], so that fp16 holds them (times 2^14; what is below 2^-39 of
-// the row's largest term is lost, a term's rounding is 2^-12 of itself).
+// in (0, 2^8], so that fp16 holds them (times 2^6; what is below 2^-31 of
+// the reference is lost, a term's rounding is 2^-12 of itself).
 //
 // What bounds it: the codes and scales of every visible position are read once
-// per cached head, 2*D*b/8 + 8 bytes a position (HBM).  Per code it can afford
-// about 3 (4 bits) to 1.5 (2 bits) lane instructions at that rate, and the G
-// query heads of a cached head share the codes: so the products run on
-// mma.sync, whose A fragments are widened in registers straight from the codes
-// (a tcgen05 operand would have to go through shared or tensor memory first; the
-// tensor rate is far from the limit here, a warp's 16 positions x D codes
-// are two m16n8k16 per 256 codes).
+// per cached head, 2*D*b/8 + 8 bytes a position (HBM), and close behind it the
+// integer unit, which masks the codes out (one operation to two lanes' worth of
+// cycles).  The G query heads of a cached head share the codes, so the products
+// run on mma.sync, whose A fragments are made in registers straight from the
+// codes (a tcgen05 operand would have to go through shared or tensor memory
+// first; the tensor rate is far from the limit here).  Both products run on
+// exact integers in fp16, whose ten mantissa bits take two 4-bit codes of a half
+// word unshifted (bf16: one).  Q is fp16 times a power of two of its row that
+// brings its largest value to [2^14, 2^15): values down to 2^-31 of that are
+// exact, smaller ones are off by 2^-39 of it at most.  (Codes left masked as
+// subnormal fp16, with the offset taken off the sums, save the fma, but the
+// tensor cores align such products by their exponent field and lose ten bits.)
 //
 // One CTA: one sequence, cached head, block of 8*NT rows (query heads of the
-// sequence's new tokens) and a range of positions; its warps take 32 positions
-// in turn, each through a ring of cp.async stages of its own (no CTA barrier in
+// sequence's new tokens) and a range of positions; its warps take KW positions
+// in turn, each through a ring of bulk copies of its own (no CTA barrier in
 // the loop), and join their (m, sum, O) in shared memory.  Ranges of one
-// sequence are joined by the combine kernel.
+// sequence are joined by the combine kernel.  The reference point m follows the
+// running maximum only when a score passes it by more than 2^8.
 //
 // Fragments.  Positions are the M of both products (S^T = K Q^T, 16 positions x
 // 8 rows; O^T = V^T P^T, 16 values x 8 rows), so eight rows waste nothing.
 // The contraction may run over D in any order: lane t of a quad takes D/4
-// consecutive codes of its position, in the pair order that widening gives, and
+// consecutive codes of its position, in the pair order that masking gives, and
 // Q's fragment is laid out to match.  Slot r of a block of 16 positions is
 // position (r >> 1 & 3) + 4 * (r & 1) + (r & 8), so that lane t's four V rows are t,
 // t + 4, t + 8, t + 12 (neighbouring lanes read neighbouring rows).  P^T becomes
@@ -47,36 +53,35 @@ using k12::Plan;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int KW = 32;                     // positions of one warp step
-constexpr float kShift = 14.f;             // weights are held times 2^14
+constexpr float kShift = 6.f;              // weights are held times 2^6 ...
+constexpr float kLazy = 8.f;               // ... and may pass the reference by 2^8
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 
+// A warp's step: 64 positions, fewer of long rows, so that two or three stages a
+// warp leave room for three CTAs an SM.
 template <int D, int B>
 struct Stage {
     static constexpr int kRow = D * B / 8;
+    static constexpr int KW = kRow <= 64 ? 64 : kRow <= 128 ? 32 : 16;
     static constexpr int kCodes = KW * kRow;                        // K's or V's
     static constexpr int kScales = KW * 4;
     static constexpr int kBytes = 2 * kCodes + 2 * kScales + 16;    // + the flags word
-    // stages of one warp: about 12 KB in flight, at least two
-    static constexpr int kCount = kBytes * 4 <= 20480 ? 4 : kBytes * 3 <= 26000 ? 3 : 2;
+    static constexpr int kCount = kBytes * 3 <= 14000 ? 3 : 2;
 };
 template <int D, int B, int NT>
-constexpr int smem_bytes() {
+__host__ __device__ constexpr int smem_bytes() {
     const int ring = kWarps * Stage<D, B>::kCount * Stage<D, B>::kBytes + 16;
     const int join = kWarps * 8 * NT * (D + 4) * 4 + kWarps * 8 * NT * 8;
-    return ring > join ? ring : join;
+    return (ring > join ? ring : join) + kWarps * 32;  // + the barriers
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// CTAs to an SM that the registers leave room for.
+template <int D, int NT>
+constexpr int kCtas = NT == 1 && D <= 128 ? 3 : 2;
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -84,7 +89,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 __device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
@@ -97,6 +102,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float lg2(float x) {
     float r;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -104,29 +114,48 @@ __device__ __forceinline__ float lg2(float x) {
 }
 
 template <int D, int B, int NT>
-__global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb, KvAttn a, Plan pl,
-                                                          float* part, int32_t* status) {
+__global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
+    decode_kernel(KvCache c, KvBatch kb, KvAttn a, Plan pl, float* part, int32_t* status) {
     using St = Stage<D, B>;
     constexpr int R = 8 * NT;            // rows of the block
     constexpr int NK = D / 4, NV = D / 8;  // codes of a lane's K row, of its V rows
     constexpr int kPairs = D / 8;        // K pairs of a lane
     constexpr int H = kKvHalfCodes<B>;
+    constexpr int KW = St::KW, NB = KW / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-    // ---- which rows, which positions
-    const int split = (int)(blockIdx.x % pl.splits);
-    const int rb = (int)(blockIdx.x / pl.splits % pl.row_blocks);
-    const int b = (int)(blockIdx.x / pl.splits / pl.row_blocks), h = (int)blockIdx.y;
-    const k12::Rows s = k12::rows_of(kb, c.page_size, a, b);
-    if (s.bad && split == 0 && rb == 0 && h == 0 && threadIdx.x == 0)
-        report_status(status, HBL_ERR_INVALID_ARG);
-    const int nr = s.n * a.group;  // this sequence's rows on this head
-    if (nr < pl.min_rows || nr > pl.max_rows || rb * R >= nr) return;
-    const k12::Range rg = k12::range_of(a, s, rb * R, min(nr, rb * R + R) - 1);
-    const k12::Split sp = k12::split_of(pl, rg, split);
-    if (split >= max(sp.count, 1)) return;
+    // ---- this CTA's piece of the line
+    const k12::Line line = k12::line_of<kThreads, false>(pl, c, kb, a, blockIdx.x,
+                                                         blockIdx.x == 0 ? status : nullptr);
+    int at = line.at;
+    if (at >= line.total) return;
+    const int stop = (int)min((int64_t)at + line.per, (int64_t)line.total);
     pdl_launch_dependents();
+
+    const uint32_t ring = smem_addr(smem) + warp * St::kCount * St::kBytes;
+    const uint32_t bars = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + warp * 32;
+    if (lane < St::kCount) mbar_init_count(bars + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    int done = 0;  // stages of this warp's ring that have been used
+    int item = line.item;
+    k12::Item im = k12::item_of(pl, c, kb, a, item);
+    int before = line.before;  // the line's units before this item
+    while (true) {
+    // ---- one head's part of an item: units [u0, u1) of im.units
+    while (at >= before + im.units * c.heads) {
+        before += im.units * c.heads;
+        im = k12::item_of(pl, c, kb, a, ++item);
+    }
+    const int b = item / pl.row_blocks, rb = item - b * pl.row_blocks;
+    const int h = (at - before) / im.units, u0 = (at - before) - h * im.units;
+    const int u1 = min(im.units, u0 + (stop - at));
+    at += u1 - u0;
+    const k12::Rows s = im.s;
+    const int nr = im.nr;
+    const int begin = im.from + u0 * pl.unit;
+    const int end = u1 == im.units ? im.rg.end : im.from + u1 * pl.unit;
 
     // per lane: the visible range of rows 2t, 2t + 1 of each tile
     int lo[NT][2], hi[NT][2];
@@ -149,64 +178,58 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
     }
 
     // ---- the ring of this warp
-    const uint32_t ring = smem_addr(smem) + warp * St::kCount * St::kBytes;
     const int step = kWarps * KW;
-    const int first = sp.begin + warp * KW;
-    const int steps = first < sp.end ? (sp.end - first + step - 1) / step : 0;
-    // lanes 0, 1 (and all others alike): the page of segment lane & 1 of a step
+    const int first = begin + warp * KW;
+    const int steps = first < end ? (end - first + step - 1) / step : 0;
+    // one copy takes the positions of one page: seg of them, and a lane to each of
+    // K's and V's codes and scales (lane >> 2) of each segment (lane & 3)
+    const int seg_shift = min(pl.seg_shift, ilog2(KW)), seg = 1 << seg_shift;
+    const int my_seg = lane & 3, my_kind = lane >> 2;
+    const bool copies = my_kind < 4 && my_seg < (KW >> seg_shift);
     auto page_of = [&](int it) {
-        const int key = first + it * step + 16 * (lane & 1);
-        if (it >= steps || key >= sp.end) return -2;  // nothing there
+        const int key = first + it * step + (my_seg << seg_shift);
+        if (it >= steps || !copies || key >= end) return -2;  // nothing there
         return kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
     };
+    uint8_t* const my_base = my_kind == 0 ? c.kc : my_kind == 1 ? c.vc
+                             : reinterpret_cast<uint8_t*>(my_kind == 2 ? c.ks : c.vs);
+    const int my_row = my_kind < 2 ? St::kRow : 4;
+    const uint32_t my_dst = (my_kind < 2 ? my_kind * St::kCodes
+                                         : 2 * St::kCodes + (my_kind - 2) * St::kScales) +
+                            (my_seg << seg_shift) * my_row;
     auto issue = [&](int it, int page) {
-        if (it < steps) {
-            const uint32_t st = ring + (it % St::kCount) * St::kBytes;
-            const int key = first + it * step + 16 * (lane & 1);
-            int64_t base = 0;
-            if (page >= 0)
-                base = ((int64_t)page * c.heads + h) * c.page_size +
-                       (key - (int)pl.div_page(key) * c.page_size);
-            int64_t row[2];
-            bool ok[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                row[e] = __shfl_sync(0xffffffffu, base, e);
-                ok[e] = __shfl_sync(0xffffffffu, page, e) >= 0;
-            }
-            constexpr int kChunks = 2 * St::kRow;  // 16-byte pieces: 16 rows of kRow bytes, twice
-#pragma unroll
-            for (int k = 0; k < (kChunks + 31) / 32; ++k) {
-                const int ch = lane + 32 * k;
-                if (kChunks % 32 == 0 || ch < kChunks) {
-                    const int seg = ch >= St::kRow, off = (ch - seg * St::kRow) * 16;
-                    const int64_t at = (seg ? row[1] : row[0]) * St::kRow + off;
-                    const int bytes = (seg ? ok[1] : ok[0]) ? 16 : 0;
-                    cp_async16(st + ch * 16, c.kc + at, bytes);
-                    cp_async16(st + St::kCodes + ch * 16, c.vc + at, bytes);
-                }
-            }
-            if (lane < 16) {  // the scales: 2 segments x 4 pieces, of K and of V
-                const int seg = (lane >> 2) & 1, off = (lane & 3) * 4;
-                const float* src = (lane < 8 ? c.ks : c.vs) + (seg ? row[1] : row[0]) + off;
-                cp_async16(st + 2 * St::kCodes + lane * 16, src, (seg ? ok[1] : ok[0]) ? 16 : 0);
-            }
-            if (lane == 0) {
-                const uint32_t flags = (ok[0] ? 1u : 0u) | (ok[1] ? 2u : 0u);
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * St::kCodes + 2 * St::kScales),
-                             "r"(flags)
-                             : "memory");
-            }
-            if (page == -1) report_status(status, HBL_ERR_INVALID_ARG);
+        if (it >= steps) return;
+        const int slot = (done + it) % St::kCount;
+        const uint32_t st = ring + slot * St::kBytes, bar = bars + 8 * slot;
+        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+        if (page == -1) report_status(status, HBL_ERR_INVALID_ARG);
+        if (lane == 0) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * St::kCodes + 2 * St::kScales),
+                         "r"(there & 15u)
+                         : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                         "r"((uint32_t)(__popc(there & 15u) * seg * (2 * St::kRow + 8)))
+                         : "memory");
         }
-        cp_async_commit();
+        __syncwarp();
+        if (page >= 0) {
+            const int key = first + it * step + (my_seg << seg_shift);
+            const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
+                                (key - (int)pl.div_page(key) * c.page_size);
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+                "[%3];" ::"r"(st + my_dst),
+                "l"(my_base + row * my_row), "r"((uint32_t)(seg * my_row)), "r"(bar)
+                : "memory");
+        }
     };
 #pragma unroll
-    for (int it = 0; it < St::kCount - 1; ++it) issue(it, page_of(it));
-    int next_page = page_of(St::kCount - 1);
+    for (int it = 0; it < St::kCount; ++it) issue(it, page_of(it));
+    int next_page = page_of(St::kCount);
 
     // ---- Q's fragments: pair p of lane t is codes (C w + i, C w + i + C/2), C = 2H
     uint32_t q[NT][kPairs];
+    float xs[NT][2];  // scale * log2(e) of rows 2t, 2t + 1, and their power of two taken back
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = rb * R + 8 * n + g;
@@ -222,17 +245,37 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
             raw[4 * k + 2] = v.z;
             raw[4 * k + 3] = v.w;
         }
+        float big = 0.f;
+#pragma unroll
+        for (int k = 0; k < NK / 2; ++k) {
+            const float2 f = bf16x2_to_f2(raw[k]);
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^(14 - e), e the exponent of the row's largest value
+        const int e = max((int)(__float_as_uint(big) >> 23) - 127, -112);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
         constexpr int C = NK < 2 * H ? NK : 2 * H;
         static_for<0, kPairs>([&](auto pp) {
             constexpr int p = decltype(pp)::value, w = p / (C / 2), i0 = p % (C / 2);
             constexpr int e0 = C * w + i0, e1 = e0 + C / 2;
-            q[n][p] = __byte_perm(raw[e0 / 2], raw[e1 / 2],
-                                  (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
+            auto value = [&](int x) {
+                return __uint_as_float((x & 1) ? raw[x / 2] & 0xffff0000u : raw[x / 2] << 16);
+            };
+            q[n][p] = f2_to_f16x2(value(e0) * up, value(e1) * up);
         });
+        // row 8n + g's lane holds e; lanes (., t) need rows 2t, 2t + 1
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int ee = __shfl_sync(0xffffffffu, e, (2 * t + u) * 4);
+            xs[n][u] = a.scale * 1.4426950408889634f * 0x1p-14f *
+                       __uint_as_float((uint32_t)(127 + ee) << 23);
+        }
     }
 
     float O[NV / 2][NT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], base[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -240,30 +283,37 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
 #pragma unroll
             for (int e = 0; e < 4; ++e) O[k][n][e] = 0.f;
         m[n][0] = m[n][1] = -CUDART_INF_F;
-        l[n][0] = l[n][1] = 0.f;
+        l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
     }
-    const float xscale = a.scale * 1.4426950408889634f;
     const int kslot = (g >> 1) + 4 * (g & 1);  // this lane's K rows: kslot, kslot + 8
 
-    for (int it = 0; it < steps; ++it) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(St::kCount - 2) : "memory");
-        __syncwarp();
-        issue(it + St::kCount - 1, next_page);
-        next_page = page_of(it + St::kCount);
-        const uint32_t st = ring + (it % St::kCount) * St::kBytes;
+    int it = 0;
+    for (; it < steps; ++it) {
+        const int ring_slot = (done + it) % St::kCount;
+        const uint32_t st = ring + ring_slot * St::kBytes;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded<false>(bars + 8 * ring_slot,
+                                                              ((done + it) / St::kCount) & 1, kTimeoutNs))) {
+            if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
+            break;
+        }
         const int key0 = first + it * step;
         const uint32_t flags = lds32(st + 2 * St::kCodes + 2 * St::kScales);
-        const bool plain = flags == 3u && key0 >= all_lo && key0 + KW <= min(all_hi, sp.end);
+        const bool plain = flags == (1u << (KW >> seg_shift)) - 1u && key0 >= all_lo &&
+                           key0 + KW <= min(all_hi, end);
 
-        float S[2][NT][4];
-        float rsv[2][2];  // 1 / sv of positions kslot, kslot + 8 of each block
+        // two blocks of 16 positions at a time: enough independent chains for three
+        // warps a scheduler, and half the code of the whole step (a CTA's first
+        // pass waits for its instructions)
+#pragma unroll 1
+        for (int sub = 0; sub < KW; sub += 16 * NB) {
+        float S[NB][NT][4];
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
+        for (int blk = 0; blk < NB; ++blk) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[blk][n][e] = 0.f;
-            const uint32_t r0 = st + (16 * blk + kslot) * St::kRow;
+            const uint32_t r0 = st + (sub + 16 * blk + kslot) * St::kRow;
             uint32_t w0[kKvWords<B, NK>], w1[kKvWords<B, NK>];
             kv_lds_codes<B, NK>(r0, t, w0);
             kv_lds_codes<B, NK>(r0 + 8 * St::kRow, t, w1);
@@ -275,62 +325,78 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
             static_for<0, kKvWords<B, NK>>([&](auto ww) {
                 constexpr int w = decltype(ww)::value;
                 uint32_t a0[P], a1[P];
-                kv_widen_bf16<B, P>(w0[w], a0);
-                kv_widen_bf16<B, P>(w1[w], a1);
+                kv_widen_f16<B, P>(w0[w], a0);
+                kv_widen_f16<B, P>(w1[w], a1);
 #pragma unroll
                 for (int p = 0; p < P; p += 2)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma_bf16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1], q[n][P * w + p],
-                                 q[n][P * w + p + 1]);
+                        mma_f16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1], q[n][P * w + p],
+                                q[n][P * w + p + 1]);
             });
         }
-        // ---- exponents; what is not visible becomes -inf, whatever is stored there
-        float mx[NT][2];
+        // ---- exponents
+        float mx[NT][2], rsv[NB][2];  // rsv: 1 / sv of positions kslot, kslot + 8
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -CUDART_INF_F;
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
+        for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int slot = 16 * blk + kslot + 8 * u, key = key0 + slot;
-                const uint32_t sc = st + 2 * St::kCodes + 4 * slot;
+                const uint32_t sc = st + 2 * St::kCodes + 4 * (sub + 16 * blk + kslot + 8 * u);
                 const float sk = __uint_as_float(lds32(sc));
-                const float sv = __uint_as_float(lds32(sc + St::kScales));
-                const bool there = plain || (((flags >> blk) & 1u) != 0 && key < sp.end);
-                const float ck = there ? __fmul_rn(sk, xscale) : 0.f;
                 // a zero scale (an all-zero row: its codes are zero too) as 2^-100
-                const float lv = there ? fmaxf(lg2(sv), -100.f) : 0.f;
+                const float lv = fmaxf(lg2(__uint_as_float(lds32(sc + St::kScales))), -100.f);
                 rsv[blk][u] = ex2(-lv);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = __fmaf_rn(S[blk][n][2 * u + e], ck, lv);
-                        if (!plain && !(there && key >= lo[n][e] && key < hi[n][e]))
-                            x = -CUDART_INF_F;
-                        S[blk][n][2 * u + e] = x;
-                        mx[n][e] = fmaxf(mx[n][e], x);
-                    }
+                    for (int e = 0; e < 2; ++e)
+                        S[blk][n][2 * u + e] =
+                            __fmaf_rn(S[blk][n][2 * u + e], __fmul_rn(sk, xs[n][e]), lv);
             }
+        if (!plain) {  // what is not visible becomes -inf, whatever is stored there
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int slot = sub + 16 * blk + kslot + 8 * u, key = key0 + slot;
+                    const bool there =
+                        ((flags >> (slot >> seg_shift)) & 1u) != 0 && key < end;
+                    if (!there) rsv[blk][u] = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (!(there && key >= lo[n][e] && key < hi[n][e]))
+                                S[blk][n][2 * u + e] = -CUDART_INF_F;
+                }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
+                mx[n][e] = fmaxf(S[0][n][e], S[0][n][2 + e]);
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-                    mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
-        bool grew = false;
+                for (int blk = 1; blk < NB; ++blk)
+                    mx[n][e] = max3(mx[n][e], S[blk][n][e], S[blk][n][2 + e]);
+            }
+        // each lane looks at its own positions' largest; only when one is too far
+        // above the reference do the lanes of a row find their common one
+        bool far = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) grew |= mx[n][0] > m[n][0] || mx[n][1] > m[n][1];
-        if (__any_sync(0xffffffffu, grew)) {
+        for (int n = 0; n < NT; ++n) far |= mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
+        if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
                     const float nm = fmaxf(m[n][e], mx[n][e]);
                     const float f = nm == m[n][e] ? 1.f : ex2(m[n][e] - nm);
                     m[n][e] = nm;
+                    // a row that has seen nothing: 2^(-inf) = 0 against any base
+                    base[n][e] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
                     l[n][e] *= f;
 #pragma unroll
                     for (int k = 0; k < NV / 2; ++k) {
@@ -341,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
         }
         // ---- weights and the second product
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
+        for (int blk = 0; blk < NB; ++blk) {
             uint32_t p[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -350,16 +416,14 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
                     float w[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        // a row that has seen nothing yet: 2^(-inf) = 0 against any base
-                        const float base = m[n][e] == -CUDART_INF_F ? 0.f : kShift - m[n][e];
-                        w[e] = ex2(S[blk][n][2 * u + e] + base);
+                        w[e] = ex2(S[blk][n][2 * u + e] + base[n][e]);
                         l[n][e] = __fmaf_rn(w[e], rsv[blk][u], l[n][e]);
                     }
                     p[n][u] = transpose8(f2_to_f16x2(w[0], w[1]));
                 }
-            const uint32_t r0 = st + St::kCodes + (16 * blk + t) * St::kRow;
-            constexpr int W = kKvWords<B, NV>;
-            uint32_t v[4][W];
+            const uint32_t r0 = st + St::kCodes + (sub + 16 * blk + t) * St::kRow;
+            constexpr int VW = kKvWords<B, NV>;
+            uint32_t v[4][VW];
 #pragma unroll
             for (int k = 0; k < 4; ++k) kv_lds_codes<B, NV>(r0 + 4 * k * St::kRow, g, v[k]);
             constexpr int P = NV < H ? NV : H;  // values of a half word
@@ -377,9 +441,17 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
                                 p[n][0], p[n][1]);
             });
         }
+        }
+        __syncwarp();  // the stage is read
+        issue(it + St::kCount, next_page);
+        next_page = page_of(it + St::kCount + 1);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-
+    // after a timeout: the copies still in flight, before their stages are reused
+    for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
+        mbar_wait_bounded<true>(bars + 8 * ((done + j) % St::kCount),
+                                ((done + j) / St::kCount) & 1, kTimeoutNs);
+    done += steps;
+    const bool late = it < steps;
     // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -430,13 +502,17 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(KvCache c, KvBatch kb,
             y.z = __fmaf_rn(v.z, f, y.z);
             y.w = __fmaf_rn(v.w, f, y.w);
         }
-        if (sp.count <= 1) {
+        if (u0 == 0 && u1 == im.units) {
             k12::store_row<4>(a, s, h, row, d, &y.x, M - kShift, L);
         } else {
-            float* dst = part + k12::part_index(pl, c, b, h, split, row) * (D + 4);
+            float* dst = k12::slot_of(part, pl, D, blockIdx.x, u0 == 0) + r * (D + 4);
             *reinterpret_cast<float4*>(dst + d) = y;
             if (d == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M - kShift, L);
         }
+    }
+    // the rings' memory goes back to the copies; a CTA that has lost one ends here
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (__syncthreads_or(late) || at >= stop) return;
     }
 }
 
@@ -446,8 +522,7 @@ hbl_status launch(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Pl
     constexpr int kSmem = smem_bytes<D, B, NT>();
     auto kern = decode_kernel<D, B, NT>;
     if (!smem_attr_once(reinterpret_cast<const void*>(kern), kSmem)) return HBL_ERR_CUDA;
-    const dim3 grid((unsigned)(kb.num_seqs * pl.row_blocks * pl.splits), (unsigned)c.heads);
-    kern<<<grid, kThreads, kSmem, stream>>>(c, kb, a, pl, part, status);
+    kern<<<(unsigned)pl.ctas, kThreads, kSmem, stream>>>(c, kb, a, pl, part, status);
     return cudaGetLastError() == cudaSuccess ? HBL_OK : HBL_ERR_CUDA;
 }
 

@@ -484,6 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     tmem_st_16x128b_x8(s_t + (16u << 16), p[1]);
                 }
                 tmem_wait_st();
+                // With one row set the last scores are issued before the one but last
+                // product, so that product may still be outstanding here; a parity tells
+                // neighbouring phases apart only, so it is waited for before the last
+                // product can be issued, and the wait behind the loop is for one phase.
+                if (NQ == 1 && j > 0 && j + 1 == tiles) ok = wait.all(ofull(0), (j - 1) & 1);
+                if (!ok) break;
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -494,10 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             // ---- the accumulator out, 32 columns at a time through this warp's own
             // part of the queries' tile (its rows' queries are used up: the last
             // product has landed)
-            // (With one row set the last two products may both be outstanding -- the
-            // last scores were issued before the one but last product -- and a
-            // parity tells only neighbouring phases apart: wait for each.)
-            if (NQ == 1 && tiles > 1) ok = ok && wait.all(ofull(0), (tiles - 2) & 1);
             if (ok && tiles > 0) ok = wait.all(ofull(NQ == 2 ? set : 0), (tiles - 1) & 1);
             if (ok) {
                 tmem_fence_after();

@@ -399,6 +399,19 @@ def test_attention_repeats_bit_for_bit(new, lens):
 
 
 @gpu
+@pytest.mark.parametrize("D", DIMS)
+def test_many_tiles_many_times(D):
+    # long non-causal chunks on every SM, launched back to back: no wait of the
+    # kernel's pipeline may be missed
+    c = ref.Case([17], [2100], heads=148 * 4, kv_heads=148, D=D, bits=2, page=64, seed=D)
+    status = hbl.new_status(DEV)
+    outs = [hbl.kv_attention(c.q, c.cache, *c.batch, causal=False, status=status) for _ in range(60)]
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+@gpu
 def test_rows_past_max_rows_are_left_out_and_reported():
     c = ref.Case([5, 40], [50, 60], heads=2, kv_heads=2, D=64, bits=4, seed=3)
     status = hbl.new_status(DEV)
