@@ -134,6 +134,27 @@ hbl_status kv_dispatch(int D, int bits, F&& f) {
     }
 }
 
+// ------------------------------------------------------------ waits of a pipeline
+
+// Waits for an mbarrier phase, for at most about two seconds (in SM clocks), and
+// while *abort_flag (if given) is zero.  Polls in a bare loop and looks at the flag
+// and the clock now and then only: in kernels that hand over every few hundred
+// cycles, reading the global timer at each failed poll costs more than the wait.
+__device__ __forceinline__ bool mbar_wait_clock(uint32_t bar, uint32_t parity,
+                                                const volatile int* abort_flag) {
+    constexpr int64_t kLimit = 4000000000ll;
+    int64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_test_parity(bar, parity)) return true;
+        if ((n & 127u) == 0) {
+            if (abort_flag != nullptr && *abort_flag) return false;
+            const int64_t t = clock64();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kLimit) return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------ the paged batch
 
 // One sequence of the batch: rows [r0, r1) of the packed new rows, `len`

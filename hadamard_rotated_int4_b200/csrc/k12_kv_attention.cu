@@ -59,7 +59,7 @@ __device__ __forceinline__ void join_row(const KvAttn& a, const Rows& s, int h, 
         y.z += z.z;
         y.w += z.w;
     }
-    store_row<4>(a, s, h, row, 4 * t, &y.x, M, L);
+    store_row4(a, s, h, row, 4 * t, y, M, L);
 }
 
 // Few rows: CTA (i, r) joins row r of the one head of an item that begins in piece

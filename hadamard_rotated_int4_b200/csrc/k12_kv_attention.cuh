@@ -197,30 +197,25 @@ __device__ __forceinline__ float* slot_of(float* part, const Plan& pl, int D, in
     return part + (cta * 2 + slot) * pl.block_rows * (D + 4);
 }
 
-// Values d .. d + N - 1 of a head row from its weighted sum y and sum of weights
-// L, both against 2^M; the thread with d == 0 stores the row's lse.
-template <int N>
-__device__ __forceinline__ void store_row(const KvAttn& a, const Rows& s, int h, int row, int d,
-                                          const float* y, float M, float L) {
+// Where a head row's O goes, and 1 / L of its sum of weights L (against 2^M);
+// stores the row's lse if this thread is the one to.
+__device__ __forceinline__ uint16_t* row_out(const KvAttn& a, const Rows& s, int h, int row, float M,
+                                             float L, bool store_lse, float* inv) {
     const int i = row / a.group, head = h * a.group + (row - i * a.group);
     const int64_t t = s.row0 + i;
-    const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) w[k] = f2_to_bf16x2(y[2 * k] * inv, y[2 * k + 1] * inv);
-    uint16_t* dst = a.o + t * a.o_row + (int64_t)head * a.o_head + d;
-    if constexpr (N % 8 == 0) {
-#pragma unroll
-        for (int k = 0; k < N / 8; ++k)
-            reinterpret_cast<uint4*>(dst)[k] =
-                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    } else {
-        static_assert(N == 4, "four values or whole 16-byte vectors");
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    }
-    if (d == 0 && a.lse != nullptr)
+    *inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+    if (store_lse && a.lse != nullptr)
         a.lse[t * a.heads + head] =
             L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
+    return a.o + t * a.o_row + (int64_t)head * a.o_head;
+}
+// Four values of a head row, from column d on, from their weighted sums y.
+__device__ __forceinline__ void store_row4(const KvAttn& a, const Rows& s, int h, int row, int d,
+                                           const float4& y, float M, float L) {
+    float inv;
+    uint16_t* dst = row_out(a, s, h, row, M, L, d == 0, &inv) + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(f2_to_bf16x2(y.x * inv, y.y * inv),
+                                                f2_to_bf16x2(y.z * inv, y.w * inv));
 }
 
 }  // namespace k12

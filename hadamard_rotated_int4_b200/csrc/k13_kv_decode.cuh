@@ -55,7 +55,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kShift = 6.f;              // weights are held times 2^6 ...
 constexpr float kLazy = 8.f;               // ... and may pass the reference by 2^8
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // A warp's step: 64 positions, fewer of long rows, so that two or three stages a
 // warp leave room for three CTAs an SM.
@@ -291,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
     for (; it < steps; ++it) {
         const int ring_slot = (done + it) % St::kCount;
         const uint32_t st = ring + ring_slot * St::kBytes;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded<false>(bars + 8 * ring_slot,
-                                                              ((done + it) / St::kCount) & 1, kTimeoutNs))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clock(bars + 8 * ring_slot,
+                                                     ((done + it) / St::kCount) & 1, nullptr))) {
             if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
             break;
         }
@@ -448,8 +447,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
     }
     // after a timeout: the copies still in flight, before their stages are reused
     for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
-        mbar_wait_bounded<true>(bars + 8 * ((done + j) % St::kCount),
-                                ((done + j) / St::kCount) & 1, kTimeoutNs);
+        mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
+                        nullptr);
     done += steps;
     const bool late = it < steps;
     // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
             y.w = __fmaf_rn(v.w, f, y.w);
         }
         if (u0 == 0 && u1 == im.units) {
-            k12::store_row<4>(a, s, h, row, d, &y.x, M - kShift, L);
+            k12::store_row4(a, s, h, row, d, y, M - kShift, L);
         } else {
             float* dst = k12::slot_of(part, pl, D, blockIdx.x, u0 == 0) + r * (D + 4);
             *reinterpret_cast<float4*>(dst + d) = y;

@@ -11,22 +11,27 @@
 // accumulator in tensor memory is rescaled a few times a row, not every tile.
 //
 // One CTA: one sequence, cached head and 2 x 128 head rows (128 at D = 256),
-// and a range of positions in tiles of KT.  Sixteen warps:
+// and a range of positions, widened in tiles of KT and worked on in parts of 64.
+// Sixteen warps:
 //   0..7    softmax, four warps to each 128 rows: scores out of tensor memory,
 //           weights back into it in the scores' place
 //   8..14   widen K and V codes from HBM straight into swizzled operand tiles
 //           (two stages each) and lay out the tiles' scales
-//   15      one thread issues the MMAs: S = Q K^T (both operands in shared
+//   15      issues the MMAs: S = Q K^T (both operands in shared
 //           memory), O += P V (P in tensor memory, V read down its rows, which
 //           is the transposed operand that the second product needs)
-// While one set of rows is in its softmax the tensor core works for the other.
+// Scores have two buffers a row set: part i + 1's are computed while part i is
+// in its softmax, so the softmax warps never wait for the tensor core.
 //
-// What bounds it: a tile of 128 positions is 4 * 128^3 * 2 products for the
-// two row sets, 2048 tensor cycles at D = 128, and 2 * 128 * 128 exponentials,
-// 2048 cycles of the 16-a-cycle special-function units: both at once at best.
-// Shared memory is nearly as busy (1536 cycles of MMA operand reads, 512 of
+// What bounds it: 128 positions are 4 * 128^3 * 2 products for the two row sets,
+// 2048 tensor cycles at D = 128, and 2 * 128 * 128 exponentials, 2048 cycles of
+// the 16-a-cycle special-function units: both at once at best.  Shared memory is
+// as busy (2048 cycles of MMA operand reads with scores of 64 columns, 512 of
 // operand tiles stored), which is why scores leave tensor memory in the
-// 16x256b shape: a thread then needs a quarter of a tile's scales, not all.
+// 16x256b shape: a thread then needs a quarter of a part's scales, not all.
+// (Parts of 128 with one score buffer read less, but then every part's softmax
+// waits for the product before it and the scores after that: 6270 cycles for
+// 128 positions.)
 //
 // D order.  Widening gives codes in pairs (i, i + C/2) of C; queries are laid
 // out in the same order, and O's columns are put back when it is stored.
@@ -46,7 +51,6 @@ constexpr int kConv = 7;             // widening warps
 constexpr int kConvWarp0 = 8, kMmaWarp = 15;
 constexpr float kShift = 6.f;        // weights are held times 2^6 ...
 constexpr float kLazy = 8.f;         // ... and may pass the reference by 2^8
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kScaleStages = 4;
 
 template <int D>
@@ -54,8 +58,8 @@ struct Tile {
     static constexpr int NQ = D == 256 ? 1 : 2;       // sets of 128 rows
     static constexpr int KT = D == 256 ? 64 : 128;    // positions of a tile
     static constexpr int kPanels = D >= 64 ? D / 64 : 1;  // 128-byte panels of a row
-    static constexpr int kSBuf = 2;                   // score buffers in tensor memory
-    static constexpr uint32_t kOCol = kSBuf * KT;     // first accumulator column
+    static constexpr int kParts = KT / 64;            // parts of a tile
+    static constexpr uint32_t kOCol = 256;            // first accumulator column
     static constexpr int kQ = NQ * 128 * kPanels * 128;  // bytes
     static constexpr int kStage = KT * kPanels * 128;    // one operand tile
     static constexpr int kScale = KT * 12;               // (ck, ck, lv, lv) a pair, then 1/sv
@@ -82,27 +86,35 @@ __host__ __device__ constexpr uint32_t idesc(bool bf16, bool b_mn, int N) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// MMAs and commits by the whole, converged warp, of which one lane is elected: the
+// operands are then uniform and need not be moved from one thread's registers,
+// which took some 75 cycles an MMA.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                        uint32_t accum) {
     asm volatile(
-        "{\n.reg .pred p;\n"
+        "{\n.reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(accum)
         : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                        uint32_t accum) {
     asm volatile(
-        "{\n.reg .pred p;\n"
+        "{\n.reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(accum)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t mbar) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
+        "{\n.reg .pred e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            mbar)
         : "memory");
 }
 __device__ __forceinline__ void fence_async() {
@@ -119,6 +131,11 @@ __device__ __forceinline__ void reg_dealloc() {
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ float lg2(float x) {
@@ -143,17 +160,10 @@ struct Waiter {
         return __all_sync(0xffffffffu, one(bar, parity));
     }
     __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const {
-        if (mbar_test_parity(bar, parity)) return true;
-        const uint64_t t0 = global_ns();
-        while (true) {
-            if (mbar_test_parity(bar, parity)) return true;
-            if (*abort_flag) return false;
-            if (global_ns() - t0 > kTimeoutNs) {
-                *abort_flag = 1;
-                report_status(status, HBL_ERR_TIMEOUT);
-                return false;
-            }
-        }
+        if (mbar_wait_clock(bar, parity, abort_flag)) return true;
+        if (!*abort_flag) report_status(status, HBL_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
     }
 };
 
@@ -225,22 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
     const uint32_t base_s = (raw_s + 1023u) & ~1023u;
-    uint8_t* base = smem_raw + (base_s - raw_s);
+    uint8_t* smem_base = smem_raw + (base_s - raw_s);
     const uint32_t q_s = base_s, k_s = q_s + T::kQ, v_s = k_s + 2 * T::kStage;
     const uint32_t sc_s = v_s + 2 * T::kStage, bar_s = sc_s + kScaleStages * T::kScale;
-    uint8_t* bar_p = base + (bar_s - base_s);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_p + 200);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_p + 204);
+    uint8_t* bar_p = smem_base + (bar_s - base_s);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_p + 240);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_p + 244);
     auto kfull = [&](int s) { return bar_s + 8u * s; };
     auto kempty = [&](int s) { return bar_s + 8u * (2 + s); };
     auto vfull = [&](int s) { return bar_s + 8u * (4 + s); };
     auto vempty = [&](int s) { return bar_s + 8u * (6 + s); };
     auto scfull = [&](int s) { return bar_s + 8u * (8 + s); };
     auto scempty = [&](int s) { return bar_s + 8u * (12 + s); };
-    auto sfull = [&](int s) { return bar_s + 8u * (16 + s); };
-    auto pfull = [&](int s) { return bar_s + 8u * (18 + s); };
-    auto ofull = [&](int s) { return bar_s + 8u * (20 + s); };
-    const uint32_t qfull = bar_s + 8u * 22, drain = bar_s + 8u * 23;
+    auto sfull = [&](int s) { return bar_s + 8u * (16 + s); };  // 2 * set + buffer
+    auto pfull = [&](int s) { return bar_s + 8u * (20 + s); };
+    auto ofull = [&](int set) { return bar_s + 8u * (24 + set); };
+    const uint32_t qfull = bar_s + 8u * 26, drain = bar_s + 8u * 27;
 
     // ---- which rows, which positions: the longest row blocks start first
     const int per_block = kb.num_seqs * pl.splits;
@@ -256,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     const k12::Split sp = k12::split_of(pl, rg, split);
     if (split >= max(sp.count, 1)) return;
     pdl_launch_dependents();
-    const int tiles = sp.count == 0 ? 0 : (sp.end - sp.begin + KT - 1) / KT;
+    const int parts = sp.count == 0 ? 0 : (sp.end - sp.begin + 63) / 64;
+    const int tiles = (parts + T::kParts - 1) / T::kParts;
     const int sets = NQ == 2 && nr - row0 > 128 ? 2 : 1;  // row sets that have rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -266,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             mbar_init_count(kempty(i), 1);
             mbar_init_count(vfull(i), kConv);
             mbar_init_count(vempty(i), 1);
+            mbar_init_count(ofull(i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init_count(sfull(i), 1);
             mbar_init_count(pfull(i), 4);
-            mbar_init_count(ofull(i), 1);
         }
         for (int i = 0; i < kScaleStages; ++i) {
             mbar_init_count(scfull(i), 1);
@@ -291,43 +304,55 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, status};
 
-    if (warp < 8) {
+    if (warp < kConvWarp0) {
         // ================= softmax
-        reg_alloc<184>();
+        reg_alloc<144>();
         const int set = warp >> 2, quarter = warp & 3, g = lane >> 2, t = lane & 3;
         if (set < sets) {
             // ---- this set's queries into the operand layout
             const Lane<D> ql(lane);
             const uint32_t qbase = q_s + set * 128 * T::kPanels * 128;
             constexpr int kUnits = 128 / Lane<D>::kRows;
+            // (two units' loads in flight)
 #pragma unroll 1
-            for (int u = quarter; u < kUnits; u += 4) {
-                const int row = u * Lane<D>::kRows + ql.row, r = row0 + set * 128 + row;
-                uint32_t raw[16], out[16];
-                const int i = r / a.group;
-                const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
-                                      (int64_t)(h * a.group + (r - i * a.group)) * a.q_head +
-                                      ql.group * 32;
+            for (int u0 = quarter; u0 < kUnits; u0 += 8) {
+                uint32_t raw[2][16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 v = r < nr ? reinterpret_cast<const uint4*>(src)[k]
-                                           : make_uint4(0, 0, 0, 0);
-                    raw[4 * k] = v.x;
-                    raw[4 * k + 1] = v.y;
-                    raw[4 * k + 2] = v.z;
-                    raw[4 * k + 3] = v.w;
+                for (int v = 0; v < 2; ++v) {
+                    const int u = u0 + 4 * v, row = u * Lane<D>::kRows + ql.row;
+                    const int r = row0 + set * 128 + row, i = r / a.group;
+                    const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
+                                          (int64_t)(h * a.group + (r - i * a.group)) * a.q_head +
+                                          ql.group * 32;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 z = u < kUnits && r < nr
+                                            ? reinterpret_cast<const uint4*>(src)[k]
+                                            : make_uint4(0, 0, 0, 0);
+                        raw[v][4 * k] = z.x;
+                        raw[v][4 * k + 1] = z.y;
+                        raw[v][4 * k + 2] = z.z;
+                        raw[v][4 * k + 3] = z.w;
+                    }
                 }
-                static_for<0, 16>([&](auto pp) {
-                    constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
-                    constexpr int e1 = place_of<B>(2 * decltype(pp)::value + 1);
-                    out[decltype(pp)::value] =
-                        __byte_perm(raw[e0 / 2], raw[e1 / 2],
-                                    (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
-                });
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sts128(qbase + chunk_at(128, row, ql.group, k),
-                           make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
+                for (int v = 0; v < 2; ++v) {
+                    const int u = u0 + 4 * v;
+                    if (u >= kUnits) break;
+                    uint32_t out[16];
+                    static_for<0, 16>([&](auto pp) {
+                        constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
+                        constexpr int e1 = place_of<B>(2 * decltype(pp)::value + 1);
+                        out[decltype(pp)::value] =
+                            __byte_perm(raw[v][e0 / 2], raw[v][e1 / 2],
+                                        (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
+                    });
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts128(qbase + chunk_at(128, u * Lane<D>::kRows + ql.row, ql.group, k),
+                               make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2],
+                                          out[4 * k + 3]));
+                }
             }
             fence_async();
             __syncwarp();
@@ -350,55 +375,55 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
                 min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
             }
-            float m[4];
+            float m[4], base[4];
             float2 l[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 m[k] = -CUDART_INF_F;
+                base[k] = 0.f;
                 l[k] = make_float2(0.f, 0.f);
             }
             const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-            const uint32_t o_t = tmem + lanes + T::kOCol + (NQ == 2 ? set * D : 0);
+            const uint32_t o_t = tmem + lanes + T::kOCol + set * D;
             bool ok = true;
 #pragma unroll 1
-            for (int j = 0; j < tiles; ++j) {
-                const int sb = NQ == 2 ? set : (j & 1);
-                const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
-                const uint32_t s_t = tmem + lanes + sb * KT;
-                const uint32_t sc = sc_s + (j % kScaleStages) * T::kScale;
-                ok = wait.all(scfull(j % kScaleStages), (j / kScaleStages) & 1) && wait.all(sfull(sb), par);
+            for (int i = 0; i < parts; ++i) {
+                const int sb = 2 * set + (i & 1), j = i / T::kParts;
+                const uint32_t s_t = tmem + lanes + sb * 64;
+                // this thread's scales of the part: (ck, ck, lv, lv) and 1/sv of columns
+                // 8k + 2t, 8k + 2t + 1
+                const uint8_t* const sc_p =
+                    smem_base + (sc_s - base_s) + (j % kScaleStages) * T::kScale;
+                const float4* const sc4 =
+                    reinterpret_cast<const float4*>(sc_p + (i % T::kParts) * 512) + t;
+                const float2* const rs2 =
+                    reinterpret_cast<const float2*>(sc_p + KT * 8 + (i % T::kParts) * 256) + t;
+                ok = wait.all(scfull(j % kScaleStages), (j / kScaleStages) & 1) &&
+                     wait.all(sfull(sb), (i >> 1) & 1);
                 if (!ok) break;
                 tmem_fence_after();
-                float x[2][KT / 2];
-                if constexpr (KT == 128) {
-                    tmem_ld_16x256b_x16(s_t, x[0]);
-                    tmem_ld_16x256b_x16(s_t + (16u << 16), x[1]);
-                } else {
-                    tmem_ld_16x256b_x8(s_t, x[0]);
-                    tmem_ld_16x256b_x8(s_t + (16u << 16), x[1]);
-                }
+                float x[2][32];
+                tmem_ld_16x256b_x8(s_t, x[0]);
+                tmem_ld_16x256b_x8(s_t + (16u << 16), x[1]);
                 tmem_wait_ld(x[0]);
                 tmem_wait_ld(x[1]);
                 // ---- exponents
-                const int key0 = sp.begin + j * KT;
-                const bool masked = key0 < max_lo || key0 + KT > min_hi;
-                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                const int key0 = sp.begin + i * 64;
 #pragma unroll
-                for (int k = 0; k < KT / 8; ++k) {
-                    const uint4 f = lds128(sc + (4 * k + t) * 16);
-                    const float2 ck = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
-                    const float2 lv = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+                for (int k = 0; k < 8; ++k) {
+                    const float4 f = sc4[4 * k];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         float* v = &x[r >> 1][4 * k + 2 * (r & 1)];
-                        const float2 y = __ffma2_rn(make_float2(v[0], v[1]), ck, lv);
+                        const float2 y = __ffma2_rn(make_float2(v[0], v[1]), make_float2(f.x, f.y),
+                                                    make_float2(f.z, f.w));
                         v[0] = y.x;
                         v[1] = y.y;
                     }
                 }
-                if (masked) {
+                if (key0 < max_lo || key0 + 64 > min_hi) {
 #pragma unroll
-                    for (int k = 0; k < KT / 8; ++k)
+                    for (int k = 0; k < 8; ++k)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -408,32 +433,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                                     x[r >> 1][4 * k + 2 * (r & 1) + e] = -CUDART_INF_F;
                             }
                 }
-#pragma unroll
-                for (int k = 0; k < KT / 8; ++k)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        mx[r] = fmaxf(mx[r], fmaxf(x[r >> 1][4 * k + 2 * (r & 1)],
-                                                   x[r >> 1][4 * k + 2 * (r & 1) + 1]));
+                // each lane looks at its own columns' largest; only when one is too far
+                // above the reference do the lanes of a row find their common one
+                float mx[4];
                 bool far = false;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                    // a row that has seen nothing: its sums are zero, any reference will do
-                    if (m[r] == -CUDART_INF_F) m[r] = mx[r];
+                    mx[r] = fmaxf(x[r >> 1][2 * (r & 1)], x[r >> 1][2 * (r & 1) + 1]);
+#pragma unroll
+                    for (int k = 1; k < 8; ++k)
+                        mx[r] = max3(mx[r], x[r >> 1][4 * k + 2 * (r & 1)],
+                                     x[r >> 1][4 * k + 2 * (r & 1) + 1]);
                     far |= mx[r] > m[r] + kLazy;
                 }
                 if (__any_sync(0xffffffffu, far)) {
                     float f[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
                         const float nm = fmaxf(m[r], mx[r]);
                         f[r] = nm == m[r] ? 1.f : ex2(m[r] - nm);
                         m[r] = nm;
+                        // a row that has seen nothing: 2^(-inf) = 0 against any base
+                        base[r] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
                         l[r] = __fmul2_rn(l[r], make_float2(f[r], f[r]));
                     }
-                    if (j > 0) {  // the accumulator, once the product before has landed
-                        ok = wait.all(ofull(NQ == 2 ? set : 0), (j - 1) & 1);
+                    if (i > 0) {  // the accumulator, once the product before has landed
+                        ok = wait.all(ofull(set), (i - 1) & 1);
                         if (!ok) break;
                         tmem_fence_after();
 #pragma unroll 1
@@ -453,57 +480,44 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     }
                 }
                 // ---- weights
-                float2 base2[4];
+                uint32_t p[2][16];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float z = m[r] == -CUDART_INF_F ? 0.f : kShift - m[r];
-                    base2[r] = make_float2(z, z);
-                }
-                uint32_t p[2][KT / 4];
-#pragma unroll
-                for (int k = 0; k < KT / 8; ++k) {
-                    float2 rs;
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                                 : "=f"(rs.x), "=f"(rs.y)
-                                 : "r"(sc + KT * 8 + (4 * k + t) * 8)
-                                 : "memory");
+                for (int k = 0; k < 8; ++k) {
+                    const float2 rs = rs2[4 * k];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float* v = &x[r >> 1][4 * k + 2 * (r & 1)];
-                        const float2 y = __fadd2_rn(make_float2(v[0], v[1]), base2[r]);
+                        const float2 y = __fadd2_rn(make_float2(v[0], v[1]),
+                                                    make_float2(base[r], base[r]));
                         const float2 w = make_float2(ex2(y.x), ex2(y.y));
                         l[r] = __ffma2_rn(w, rs, l[r]);
                         p[r >> 1][2 * k + (r & 1)] = f2_to_f16x2(w.x, w.y);
                     }
                 }
-                if constexpr (KT == 128) {
-                    tmem_st_16x128b_x16(s_t, p[0]);
-                    tmem_st_16x128b_x16(s_t + (16u << 16), p[1]);
-                } else {
-                    tmem_st_16x128b_x8(s_t, p[0]);
-                    tmem_st_16x128b_x8(s_t + (16u << 16), p[1]);
-                }
+                tmem_st_16x128b_x8(s_t, p[0]);
+                tmem_st_16x128b_x8(s_t + (16u << 16), p[1]);
                 tmem_wait_st();
-                // With one row set the last scores are issued before the one but last
-                // product, so that product may still be outstanding here; a parity tells
-                // neighbouring phases apart only, so it is waited for before the last
-                // product can be issued, and the wait behind the loop is for one phase.
-                if (NQ == 1 && j > 0 && j + 1 == tiles) ok = wait.all(ofull(0), (j - 1) & 1);
+                // The last scores are issued before the one but last product, so that
+                // product may still be outstanding here; a parity tells neighbouring
+                // phases apart only, so it is waited for before the last product can be
+                // issued, and the wait behind the loop is for one phase.
+                if (i > 0 && i + 1 == parts) ok = wait.all(ofull(set), (i - 1) & 1);
                 if (!ok) break;
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive_one(pfull(sb));
-                    mbar_arrive_one(scempty(j % kScaleStages));
+                    if (i % T::kParts == T::kParts - 1 || i + 1 == parts)
+                        mbar_arrive_one(scempty(j % kScaleStages));
                 }
             }
             // ---- the accumulator out, 32 columns at a time through this warp's own
             // part of the queries' tile (its rows' queries are used up: the last
             // product has landed)
-            if (ok && tiles > 0) ok = wait.all(ofull(NQ == 2 ? set : 0), (tiles - 1) & 1);
+            if (ok && parts > 0) ok = wait.all(ofull(set), (parts - 1) & 1);
             if (ok) {
                 tmem_fence_after();
-                float* stage = reinterpret_cast<float*>(base + (qbase - base_s)) + quarter * 1024;
+                float* stage = reinterpret_cast<float*>(smem_base + (qbase - base_s)) + quarter * 512;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float z = l[r].x + l[r].y;
@@ -511,13 +525,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     z += __shfl_xor_sync(0xffffffffu, z, 2);
                     l[r].x = z;
                 }
-                const int myrow0 = row0 + set * 128 + 32 * quarter;
+                // this lane's rows on the way out, 16 hf + 4 i + lane / 8, and its four columns
+                constexpr int N = 8;
+                const int col = (lane & 7) * 4;
+                void* dst[N];
+                float inv[N];
+                bool there[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    // row 8k + g's sums sit in lane 4g
+                    const int k = n >> 1, from = (4 * (n & 1) + (lane >> 3)) * 4;
+                    const float L = __shfl_sync(0xffffffffu, l[k].x, from);
+                    const float M = __shfl_sync(0xffffffffu, m[k], from) - kShift;
+                    const int row = row0 + set * 128 + 32 * quarter + 4 * n + (lane >> 3);
+                    there[n] = row < nr;
+                    if (sp.count <= 1) {
+                        dst[n] = k12::row_out(a, s, h, row, M, L, there[n] && col == 0, &inv[n]) +
+                                 col;
+                    } else {
+                        float* to = part + k12::part_index(pl, c, b, h, split, row) * (D + 4);
+                        if (there[n] && col == 0)
+                            *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
+                        dst[n] = to + col;
+                        inv[n] = 1.f;
+                    }
+                }
 #pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {
+                for (int cc = 0; cc < D / 32; ++cc)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         float o[16];
-                        if (tiles > 0) {
+                        if (parts > 0) {
                             tmem_ld_16x256b_x4(o_t + ((uint32_t)(16 * hf) << 16) + 32 * cc, o);
                             tmem_wait_ld(o);
                         } else {
@@ -526,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                         }
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const int rr = 16 * hf + 8 * u + g;
+                            const int rr = 8 * u + g;  // of these 16 rows
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -537,123 +575,79 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                                     stage[rr * 32 + (d ^ ((rr & 7) * 4))] = o[4 * k + 2 * u + e];
                                 }
                         }
-                    }
-                    __syncwarp();
-                    static_for<0, 4>([&](auto kk) {
-                        constexpr int k = decltype(kk)::value;
-                        // rows 8k .. 8k + 7, whose sums are row k's of lanes 0, 4, ..
+                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int rr = 8 * k + 4 * i + (lane >> 3), d = (lane & 7) * 4;
-                            const float L = __shfl_sync(0xffffffffu, l[k].x, (4 * i + (lane >> 3)) * 4);
-                            const float M = __shfl_sync(0xffffffffu, m[k], (4 * i + (lane >> 3)) * 4);
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 4 * i + (lane >> 3), n = 4 * hf + i;
                             const float4 y = *reinterpret_cast<const float4*>(
-                                stage + rr * 32 + (d ^ ((rr & 7) * 4)));
-                            const int row = myrow0 + rr;
-                            if (row < nr) {
-                                if (sp.count <= 1) {
-                                    k12::store_row<4>(a, s, h, row, 32 * cc + d, &y.x, M - kShift,
-                                                      L);
-                                } else {
-                                    float* dst =
-                                        part + k12::part_index(pl, c, b, h, split, row) * (D + 4);
-                                    *reinterpret_cast<float4*>(dst + 32 * cc + d) = y;
-                                    if (cc == 0 && d == 0)
-                                        *reinterpret_cast<float2*>(dst + D) =
-                                            make_float2(M - kShift, L);
-                                }
-                            }
+                                stage + rr * 32 + (col ^ ((rr & 7) * 4)));
+                            if (!there[n]) continue;
+                            if (sp.count <= 1)
+                                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst[n]) + 32 * cc) =
+                                    make_uint2(f2_to_bf16x2(y.x * inv[n], y.y * inv[n]),
+                                               f2_to_bf16x2(y.z * inv[n], y.w * inv[n]));
+                            else
+                                *reinterpret_cast<float4*>(static_cast<float*>(dst[n]) + 32 * cc) = y;
                         }
-                    });
-                    __syncwarp();
-                }
+                        __syncwarp();
+                    }
             }
         }
     } else {
-        reg_dealloc<72>();
+        reg_dealloc<112>();
         if (warp == kMmaWarp) {
             // ================= MMA issue
-            if (lane == 0 && tiles > 0) {
-                constexpr uint32_t kIdQk = idesc(true, false, KT), kIdPv = idesc(false, true, D);
+            if (parts > 0) {
+                constexpr uint32_t kIdQk = idesc(true, false, 64), kIdPv = idesc(false, true, D);
                 constexpr uint32_t kPanel = KT * 128;
-                auto qk = [&](int set, int sb, int stage) {
-                    const uint32_t qa = q_s + set * 128 * T::kPanels * 128;
-                    const uint32_t ka = k_s + stage * T::kStage;
+                const uint64_t q_d = desc_k(q_s), k_d = desc_k(k_s), v_d = desc_v(v_s, kPanel);
+                // bytes to descriptor units
+                auto units = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
+                // scores of part i (64 rows of its tile's keys, score buffer i & 1) for both
+                // sets; a tile's keys are done with its last part
+                auto scores = [&](int i) {
+                    const int j = i / T::kParts;
+                    if (i % T::kParts == 0 && !wait.all(kfull(j & 1), (j >> 1) & 1)) return false;
+                    tmem_fence_after();
+                    const uint64_t b0 = k_d + units((uint32_t)(j & 1) * T::kStage +
+                                                    (uint32_t)(i % T::kParts) * 8192);
+                    for (int set = 0; set < sets; ++set) {
+                        const uint32_t sb = (uint32_t)(2 * set + (i & 1));
+                        const uint64_t a0 = q_d + units((uint32_t)set * 128 * T::kPanels * 128);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + sb * KT, desc_k(qa + (k / 4) * 128 * 128) + 2 * (k % 4),
-                               desc_k(ka + (k / 4) * kPanel) + 2 * (k % 4), kIdQk, k != 0);
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ss(tmem + sb * 64, a0 + units((k / 4) * 128 * 128) + 2 * (k % 4),
+                                   b0 + units((k / 4) * kPanel) + 2 * (k % 4), kIdQk, k != 0);
+                        commit(sfull(sb));
+                    }
+                    if (i % T::kParts == T::kParts - 1) commit(kempty(j & 1));
+                    return true;
                 };
-                auto pv = [&](int set, int sb, int stage, bool first) {
-                    const uint32_t va = v_s + stage * T::kStage;
-#pragma unroll
-                    for (int k = 0; k < KT / 16; ++k)
-                        mma_ts(tmem + T::kOCol + set * D, tmem + sb * KT + 8 * k,
-                               desc_v(va + k * 2048, kPanel), kIdPv, !(first && k == 0));
-                };
-                bool ok = wait.one(qfull, 0) && wait.one(kfull(0), 0);
-                tmem_fence_after();
-                if constexpr (NQ == 2) {
-                    if (ok) {
-                        for (int set = 0; set < sets; ++set) {
-                            qk(set, set, 0);
-                            commit(sfull(set));
-                        }
-                        commit(kempty(0));
-                    }
-                    for (int j = 0; j < tiles && ok; ++j) {
-                        const int st = j & 1, nx = st ^ 1;
-                        const uint32_t par = (j >> 1) & 1, npar = ((j + 1) >> 1) & 1;
-                        ok = wait.one(vfull(st), par);
-                        for (int set = 0; set < sets && ok; ++set) {
-                            ok = wait.one(pfull(set), j & 1);
-                            if (!ok) break;
-                            tmem_fence_after();
-                            pv(set, set, st, j == 0);
-                            commit(ofull(set));
-                            if (j + 1 < tiles) {
-                                if (set == 0) ok = wait.one(kfull(nx), npar);
-                                if (!ok) break;
-                                tmem_fence_after();
-                                qk(set, set, nx);
-                                commit(sfull(set));
-                            }
-                        }
-                        if (ok) {
-                            commit(vempty(st));
-                            if (j + 1 < tiles) commit(kempty(nx));
-                        }
-                    }
-                } else {
-                    if (ok) {
-                        qk(0, 0, 0);
-                        commit(sfull(0));
-                        commit(kempty(0));
-                    }
-                    for (int j = 0; j < tiles && ok; ++j) {
-                        const int st = j & 1, nx = st ^ 1;
-                        const uint32_t par = (j >> 1) & 1, npar = ((j + 1) >> 1) & 1;
-                        if (j + 1 < tiles) {
-                            // its score buffer held the weights of tile j - 1, whose
-                            // product was issued before
-                            ok = wait.one(kfull(nx), npar);
-                            if (!ok) break;
-                            tmem_fence_after();
-                            qk(0, nx, nx);
-                            commit(sfull(nx));
-                            commit(kempty(nx));
-                        }
-                        ok = wait.one(vfull(st), par) && wait.one(pfull(st), par);
+                bool ok = wait.all(qfull, 0) && scores(0);
+                for (int i = 0; i < parts && ok; ++i) {
+                    // part i + 1's buffer held the weights of part i - 1, whose product was
+                    // issued before
+                    if (i + 1 < parts) ok = scores(i + 1);
+                    const int j = i / T::kParts;
+                    if (ok && i % T::kParts == 0) ok = wait.all(vfull(j & 1), (j >> 1) & 1);
+                    const uint64_t b0 = v_d + units((uint32_t)(j & 1) * T::kStage +
+                                                    (uint32_t)(i % T::kParts) * 8192);
+                    for (int set = 0; set < sets && ok; ++set) {
+                        const uint32_t sb = (uint32_t)(2 * set + (i & 1));
+                        ok = wait.all(pfull(sb), (i >> 1) & 1);
                         if (!ok) break;
                         tmem_fence_after();
-                        pv(0, st, st, j == 0);
-                        commit(ofull(0));
-                        commit(vempty(st));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(tmem + T::kOCol + set * D, tmem + sb * 64 + 8 * k,
+                                   b0 + units(k * 2048), kIdPv, i != 0 || k != 0);
+                        commit(ofull(set));
                     }
+                    if (ok && i % T::kParts == T::kParts - 1) commit(vempty(j & 1));
                 }
                 // every MMA issued has completed once this commit arrives
                 commit(drain);
-                if (!mbar_wait_bounded<true>(drain, 0, kTimeoutNs))
+                if (!mbar_wait_clock(drain, 0, nullptr) && lane == 0)
                     report_status(status, HBL_ERR_TIMEOUT);
             }
         } else if (tiles > 0) {
@@ -661,17 +655,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             const int cw = warp - kConvWarp0;
             const Lane<D> ln(lane);
             uint32_t raw[T::kMine][B];
+            int page[2][T::kMine];  // of the units that are loaded next: keys, values
             // this warp's i-th unit of a tile of K (values: V's are dealt out from
             // another warp on, so that all get about the same)
             auto unit = [&](bool val, int i) { return (val ? (cw + 5) % kConv : cw) + kConv * i; };
-            auto load = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
-                const int u = unit(phase & 1, i);
-                const int key = sp.begin + (phase >> 1) * KT + u * Lane<D>::kRows + ln.row;
-                int page = -1;
-                if (u < T::kUnits && key < sp.end)
-                    page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
-                if (page >= 0) {
-                    const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
+            auto key_of = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
+                return sp.begin + (phase >> 1) * KT + unit(phase & 1, i) * Lane<D>::kRows + ln.row;
+            };
+            auto load_page = [&](int phase, int i) {
+                const int key = key_of(phase, i);
+                page[phase & 1][i] = unit(phase & 1, i) < T::kUnits && key < sp.end
+                                         ? kv_page(kb, c.num_pages, b, (int)pl.div_page(key))
+                                         : -1;
+            };
+            // the codes of a unit, whose page was looked up two phases ago
+            auto load = [&](int phase, int i) {
+                const int key = key_of(phase, i), pg = page[phase & 1][i];
+                if (pg >= 0) {
+                    const int64_t row = ((int64_t)pg * c.heads + h) * c.page_size +
                                         (key - (int)pl.div_page(key) * c.page_size);
                     const uint8_t* src = ((phase & 1) ? c.vc : c.kc) + row * ROW_BYTES +
                                          ln.group * (4 * B);
@@ -697,14 +698,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
 #pragma unroll
                     for (int k = 0; k < B; ++k) raw[i][k] = 0;
                 }
+                load_page(phase + 2, i);
             };
+            uint32_t lane_at[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) lane_at[k] = chunk_at(KT, ln.row, ln.group, k);
             auto store = [&](auto bf16, int i, int u, uint32_t dst) {
                 uint32_t out[16];
                 widen32<B, decltype(bf16)::value>(raw[i], out);
-                const int row = u * Lane<D>::kRows + ln.row;
+                // (row & 7, which the swizzle goes by, is the lane's own where a unit
+                // has a multiple of eight rows, and flips bit 2 in odd units of four)
+                const uint32_t to = dst + u * Lane<D>::kRows * 128;
+                const uint32_t flip = Lane<D>::kRows % 8 == 0 ? 0u : (uint32_t)(u & 1) << 6;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sts128(dst + chunk_at(KT, row, ln.group, k),
+                    sts128(to + (lane_at[k] ^ flip),
                            make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
             };
             const float xscale = a.scale * 1.4426950408889634f;
@@ -749,6 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             };
             const bool scales = cw == kConv - 1;
             if (scales) load_scales(0);
+#pragma unroll
+            for (int i = 0; i < T::kMine; ++i) {
+                load_page(0, i);
+                load_page(1, i);
+            }
 #pragma unroll
             for (int i = 0; i < T::kMine; ++i) load(0, i);
             bool ok = true;
