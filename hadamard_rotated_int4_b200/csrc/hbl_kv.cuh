@@ -165,9 +165,9 @@ struct KvSeq {
     int r0, r1, len;
     bool bad;
 };
-__device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {
+__device__ __forceinline__ KvSeq kv_seq_checked(const KvBatch& kb, int page_size, int c0, int c1,
+                                                int n) {
     KvSeq s;
-    const int c0 = __ldg(kb.cu + b), c1 = __ldg(kb.cu + b + 1), n = __ldg(kb.lens + b);
     s.r0 = min(max(c0, 0), kb.rows);
     s.r1 = min(max(c1, s.r0), kb.rows);
     const int64_t cap = (int64_t)kb.pages_per_seq * page_size;
@@ -175,18 +175,43 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b)
     s.bad = s.r0 != c0 || s.r1 != c1 || s.len != n;
     return s;
 }
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {
+    return kv_seq_checked(kb, page_size, __ldg(kb.cu + b), __ldg(kb.cu + b + 1),
+                          __ldg(kb.lens + b));
+}
 
 // The sequence of packed row t, found by the whole warp (every lane calls it
-// with the same t): the number of sequences whose rows end at or before t.
-// kb.num_seqs for a row behind the last sequence.
-__device__ __forceinline__ int kv_seq_of_row(const KvBatch& kb, int t) {
+// with the same t): that whose rows end first behind t.  One round of loads for 32
+// sequences: their ends and lengths come together, and the found one's are handed
+// round.  b = kb.num_seqs for a row behind the last sequence; bad is set on lanes
+// that met a descriptor outside its bounds on the way.
+__device__ __forceinline__ KvSeq kv_seq_of_row(const KvBatch& kb, int page_size, int t, int* b,
+                                               bool* bad) {
     const int lane = threadIdx.x & 31;
-    int b = 0;
+    KvSeq s = {};
+    *b = kb.num_seqs;
+    int before = __ldg(kb.cu);  // where the sequences looked at begin
     for (int i = 0; i < kb.num_seqs; i += 32) {
-        const bool before = i + lane < kb.num_seqs && __ldg(kb.cu + i + lane + 1) <= t;
-        b += __popc(__ballot_sync(0xffffffffu, before));
+        const bool in = i + lane < kb.num_seqs;
+        const int end = in ? __ldg(kb.cu + i + lane + 1) : 0;
+        const int n = in ? __ldg(kb.lens + i + lane) : 0;
+        const uint32_t after = __ballot_sync(0xffffffffu, in && end > t);
+        // the descriptors are checked as they come by (a falling or far end, a length
+        // past the table), whether row t is theirs or not
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = before;
+        if (in && kv_seq_checked(kb, page_size, start, end, n).bad) *bad = true;
+        if (after != 0) {
+            const int k = __ffs(after) - 1;
+            const int c1 = __shfl_sync(0xffffffffu, end, k), len = __shfl_sync(0xffffffffu, n, k);
+            const int c0 = k > 0 ? __shfl_sync(0xffffffffu, end, k - 1) : before;
+            *b = i + k;
+            s = kv_seq_checked(kb, page_size, c0, c1, len);
+            break;
+        }
+        before = __shfl_sync(0xffffffffu, end, 31);
     }
-    return b;
+    return s;
 }
 
 // The page that holds position pos of sequence b, or -1 if the block table names

@@ -12,15 +12,18 @@
 // Both kernels are bound by HBM at large batches and by launch latency at one
 // decoding step.  A warp takes one token and 1..kSteps steps of its 2 * heads
 // head rows (K heads, then V heads; D/16 lanes a row, 16 values a lane): the
-// token's sequence, position and page are found once per warp, by one load and
-// ballot per 32 sequences instead of a chain of dependent loads.
+// token's sequence, position and page are found once per warp, by one round of
+// loads and a ballot per 32 sequences instead of a chain of dependent loads.
 #include "hbl_kv.cuh"
 
 namespace hbl {
 namespace k11 {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kSteps = 4;  // most steps of one warp task
+// CTAs to an SM, by the registers that they leave a thread: 32 warps whose four
+// steps of rows are all in flight, 48 that hold codes only.
+constexpr int kWriteCtas = 8, kReadCtas = 12;
 
 struct Task {
     int tasks_per_row;  // warp tasks of one token
@@ -39,11 +42,12 @@ __device__ __forceinline__ Place place_of(const KvCache& c, const KvBatch& kb, i
     Place p;
     p.base = 0;
     p.in_seq = p.ok = false;
-    const int b = kv_seq_of_row(kb, t);
+    int b;
+    bool bad = false;
+    const KvSeq s = kv_seq_of_row(kb, c.page_size, t, &b, &bad);
+    if (bad) report_status(status, HBL_ERR_INVALID_ARG);
     if (b >= kb.num_seqs) return p;  // behind the last sequence
-    const KvSeq s = kv_seq(kb, c.page_size, b);
     const int pos = s.len - (s.r1 - s.r0) + (t - s.r0);
-    bool bad = s.bad;
     p.in_seq = t >= s.r0 && t < s.r1;
     if (p.in_seq && pos >= 0) {
         const int pi = pos / c.page_size;
@@ -51,16 +55,23 @@ __device__ __forceinline__ Place place_of(const KvCache& c, const KvBatch& kb, i
         if (page >= 0) {
             p.base = (int64_t)page * c.heads * c.page_size + (pos - pi * c.page_size);
             p.ok = true;
-        } else {
-            bad = true;
+        } else if ((threadIdx.x & 31) == 0) {
+            report_status(status, HBL_ERR_INVALID_ARG);
         }
     }
-    if (bad && (threadIdx.x & 31) == 0) report_status(status, HBL_ERR_INVALID_ARG);
     return p;
 }
 
+// The descriptors that the rows' own searches, 32 sequences at a time, may not come
+// to, looked over by the first warp of the grid behind its own rows.
+__device__ __forceinline__ void check_batch(const KvCache& c, const KvBatch& kb, int32_t* status) {
+    if (blockIdx.x != 0 || threadIdx.x >= 32) return;
+    for (int b = 32 + threadIdx.x; b < kb.num_seqs; b += 32)
+        if (kv_seq(kb, c.page_size, b).bad) report_status(status, HBL_ERR_INVALID_ARG);
+}
+
 template <int D, int B>
-__global__ void __launch_bounds__(kThreads) write_kernel(KvCache c, KvBatch kb, KvStates x,
+__global__ void __launch_bounds__(kThreads, kWriteCtas) write_kernel(KvCache c, KvBatch kb, KvStates x,
                                                          float eps, Task k, int32_t* status) {
     constexpr int LPR = D / kKvVpl;
     constexpr int RPW = 32 / LPR;
@@ -72,31 +83,31 @@ __global__ void __launch_bounds__(kThreads) write_kernel(KvCache c, KvBatch kb, 
         const int t = (int)(task / k.tasks_per_row);
         const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
         const int last = min(first + k.per_task, 2 * c.heads);
-        uint4 raw[2][2];
-        auto load = [&](int r, uint4 (&v)[2]) {  // head row r: K heads, then V heads
+        uint4 raw[kSteps][2];
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {  // the rows load while their place is found
+            const int r = first + step * RPW + sub;  // K heads, then V heads
             const bool isv = r >= c.heads;
             const uint16_t* src = isv ? x.v + (int64_t)t * x.v_row + (int64_t)(r - c.heads) * x.v_head
                                       : x.k + (int64_t)t * x.k_row + (int64_t)r * x.k_head;
             const uint4* s = reinterpret_cast<const uint4*>(src + li * kKvVpl);
-            v[0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
-            v[1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
-        };
-        load(first + sub, raw[0]);  // the rows load while the token's place is found
+            raw[step][0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
+            raw[step][1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
+        }
         const Place p = place_of(c, kb, t, status);
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
-            const int r0 = first + step * RPW;
-            if (r0 >= last) break;
-            if (step + 1 < kSteps && r0 + RPW < last) load(r0 + RPW + sub, raw[(step + 1) & 1]);
-            const int r = r0 + sub;
+            if (first + step * RPW >= last) break;
+            const int r = first + step * RPW + sub;
             KvHalf<B> h[2];
-            const float scale = kv_quant16<D, B>(raw[step & 1], eps, h);
+            const float scale = kv_quant16<D, B>(raw[step], eps, h);
             const bool ok = p.ok && r < last, isv = r >= c.heads;
             const int64_t row = p.base + (int64_t)(isv ? r - c.heads : r) * c.page_size;
             kv_store16<B>((isv ? c.vc : c.kc) + row * ROW_BYTES, li, h, ok);
             if (ok && li == 0) (isv ? c.vs : c.ks)[row] = scale;
         }
     }
+    check_batch(c, kb, status);
 }
 
 // value = (u - 2^(B-1)) * scale, one fp32 rounding, then one to bf16.
@@ -111,7 +122,7 @@ __device__ __forceinline__ void values16(const KvHalf<B> (&h)[2], float scale, f
 }
 
 template <int D, int B, bool F32>
-__global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, KvBatch kb, void* k_out,
+__global__ void __launch_bounds__(kThreads, kReadCtas) read_kernel(KvCache c, KvBatch kb, void* k_out,
                                                         void* v_out, Task k, int32_t* status) {
     constexpr int LPR = D / kKvVpl;
     constexpr int RPW = 32 / LPR;
@@ -141,28 +152,50 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvCache c, KvBatch kb, v
         }
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
+            if (first + step * RPW >= last) break;
             const int r = first + step * RPW + sub;
-            if (r >= last) continue;
             const bool isv = r >= c.heads;
             float v[16];
             values16<B>(h[step], scale[step], v);
-            const int64_t at =
-                ((int64_t)t * c.heads + (isv ? r - c.heads : r)) * D + li * kKvVpl;
+            uint32_t w[F32 ? 16 : 8];
             if constexpr (F32) {
-                float4* dst = reinterpret_cast<float4*>((float*)(isv ? v_out : k_out) + at);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
             } else {
-                uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(v[2 * i], v[2 * i + 1]);
-                uint4* dst = reinterpret_cast<uint4*>((uint16_t*)(isv ? v_out : k_out) + at);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            // A lane's 16-byte pieces are the halves of whole 32-byte sectors.  Two lanes
+            // trade halves, so that one store writes both halves of a sector: the even
+            // lane's sector first, then the odd lane's.
+            const bool odd = li & 1;
+            uint4* const row = reinterpret_cast<uint4*>(
+                (isv ? static_cast<uint8_t*>(v_out) : static_cast<uint8_t*>(k_out)) +
+                ((int64_t)t * c.heads + (isv ? r - c.heads : r)) * D * (F32 ? 4 : 2));
+            constexpr int kSectors = F32 ? 2 : 1;  // of a lane
+#pragma unroll
+            for (int k = 0; k < kSectors; ++k) {
+                uint32_t mine[4], theirs[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = w[8 * k + i], hi = w[8 * k + 4 + i];
+                    mine[i] = odd ? hi : lo;
+                    theirs[i] = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+                }
+                const int even_at = (li & ~1) * 2 * kSectors + 2 * k + (odd ? 1 : 0);
+                const int odd_at = even_at + 2 * kSectors;
+                if (r < last) {
+                    // even lane: its own low half, then the odd lane's; odd lane: the even
+                    // lane's high half, then its own
+                    row[even_at] = odd ? make_uint4(theirs[0], theirs[1], theirs[2], theirs[3])
+                                       : make_uint4(mine[0], mine[1], mine[2], mine[3]);
+                    row[odd_at] = odd ? make_uint4(mine[0], mine[1], mine[2], mine[3])
+                                      : make_uint4(theirs[0], theirs[1], theirs[2], theirs[3]);
+                }
             }
         }
     }
+    check_batch(c, kb, status);
 }
 
 // Few head rows in all: one step a warp, for the most warps in flight.  Many:
@@ -180,7 +213,7 @@ static Task plan(const KvCache& c, const KvBatch& b, int num_sms, unsigned* grid
     k.tasks_per_row = (int)((head_rows + k.per_task - 1) / k.per_task);
     k.tasks = (int64_t)b.rows * k.tasks_per_row;
     const int64_t ctas = (k.tasks + kThreads / 32 - 1) / (kThreads / 32);
-    *grid = (unsigned)(ctas < (int64_t)num_sms * 64 ? ctas : (int64_t)num_sms * 64);
+    *grid = (unsigned)(ctas < (int64_t)num_sms * 128 ? ctas : (int64_t)num_sms * 128);
     return k;
 }
 
