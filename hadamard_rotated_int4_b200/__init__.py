@@ -472,12 +472,12 @@ def _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows):
     """hbl_kv_batch of int32 CUDA tensors on the cache's device."""
     import torch
 
-    i32 = torch.int32
-    _dev(cu_seqlens, i32, "cu_seqlens")
-    _dev(kv_lens, i32, "kv_lens")
-    _dev(block_table, i32, "block_table")
-    if not cu_seqlens.device == kv_lens.device == block_table.device == cache.device:
-        raise ValueError("cu_seqlens, kv_lens and block_table must be on the cache's device")
+    i32, device = torch.int32, cache.device
+    for t in (cu_seqlens, kv_lens, block_table):
+        if not isinstance(t, torch.Tensor) or t.dtype is not i32 or t.device != device or \
+                not t.is_contiguous():
+            _dev(t, i32, "each of cu_seqlens, kv_lens and block_table")
+            raise ValueError("cu_seqlens, kv_lens and block_table must be on the cache's device")
     n, cu, table = kv_lens.shape, cu_seqlens.shape, block_table.shape
     if len(n) != 1 or len(cu) != 1 or len(table) != 2 or cu[0] != n[0] + 1 or table[0] != n[0]:
         raise ValueError("kv_lens must be [seqs], cu_seqlens [seqs + 1] and block_table "
@@ -490,11 +490,12 @@ def _kv_rows(t, cache, name, heads=None):
     """Checks a strided bf16 [rows, heads, D] tensor; returns its strides."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if t.device != cache.device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or \
+            t.device != cache.device:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
         raise ValueError("%s must be on the cache's device" % name)
     shape = t.shape
     if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
@@ -510,7 +511,8 @@ def _kv_call(what, cache, *args):
     """Calls the library on the cache's device and that device's current stream."""
     import torch
 
-    lib()
+    if _lib is None:
+        lib()
     index = cache._index
     stream = torch._C._cuda_getCurrentRawStream(index)
     if index == torch._C._cuda_getDevice():
@@ -560,7 +562,9 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
             raise TypeError("dtype must be torch.bfloat16 or torch.float32, got %s" % dtype)
         if rows < 0:
             raise ValueError("rows must not be negative")
-        K = torch.empty(shape, dtype=dtype, device=cache.device)
+        like = cache.k_scales if dtype is torch.float32 else None
+        K = like.new_empty(shape) if like is not None else \
+            torch.empty(shape, dtype=dtype, device=cache.device)
         V = torch.empty_like(K)
     else:
         K, V = out
@@ -578,7 +582,8 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
 
 
 def _kv_attention_bytes(cache_args, batch, args):
-    lib()
+    if _lib is None:
+        lib()
     need = ctypes.c_size_t(0)
     _check(_kv_calls["hbl_kv_attention_workspace"](cache_args, batch, args, ctypes.byref(need)),
            "hbl_kv_attention_workspace")
@@ -608,12 +613,12 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     q_row, q_head = _kv_rows(Q, cache, "Q")
     rows, heads, D = Q.shape
     if out is None:
-        out = torch.empty((rows, heads, D), dtype=torch.bfloat16, device=cache.device)
-    o_row, o_head = _kv_rows(out, cache, "out", heads)
-    if out.shape[0] != rows:
-        raise ValueError("out must have Q's shape")
-    lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) \
-        if want_lse else None
+        out, o_row, o_head = Q.new_empty((rows, heads, D)), heads * D, D
+    else:
+        o_row, o_head = _kv_rows(out, cache, "out", heads)
+        if out.shape[0] != rows:
+            raise ValueError("out must have Q's shape")
+    lse = cache.k_scales.new_empty((rows, heads)) if want_lse else None
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
     args = _pack_attn(Q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,
                       lse.data_ptr() if want_lse else 0, heads, max_rows or 0, max_kv or 0,
@@ -621,7 +626,7 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     if ws is None:
         nbytes = _kv_attention_bytes(cache._args, batch, args)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            ws = cache.k_codes.new_empty(nbytes)
     else:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != cache.device or \
                 not ws.is_contiguous():

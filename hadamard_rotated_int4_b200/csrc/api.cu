@@ -819,7 +819,7 @@ static KvAttn kv_attn_of(const hbl_kv_cache* c, const hbl_kv_batch* b, const hbl
     k.max_kv = a->max_kv == 0 || a->max_kv > cap ? (int)cap : a->max_kv;
     k.scale = a->scale;
     k.causal = a->causal;
-    k.window = a->window;
+    k.window = a->window < cap ? a->window : 0;  // one that long hides nothing
     return k;
 }
 

@@ -88,21 +88,27 @@ __global__ void __launch_bounds__(kThreads) join_pieces_kernel(KvCache c, KvBatc
                     2 * pl.block_rows * (D + 4));
 }
 
-// Chunks: one CTA to a head row, whose ranges of positions it joins.
+// Chunks: one CTA to a packed row and query head, whose ranges of positions it joins.
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_ranges_kernel(KvCache c, KvBatch kb, KvAttn a,
                                                                Plan pl, const float* part) {
-    const int rows = pl.row_blocks * pl.block_rows, bh = (int)(blockIdx.x / rows);
-    const int row = (int)(blockIdx.x - (int64_t)bh * rows), b = bh / c.heads, h = bh - b * c.heads;
-    const Rows s = rows_of(kb, c.page_size, a, b);
-    const int nr = s.n * a.group, r0 = row / pl.block_rows * pl.block_rows;
-    int count = 0;
-    if (row < nr && nr >= pl.min_rows && nr <= pl.max_rows)
-        count = split_of(pl, range_of(a, s, r0, min(nr, r0 + pl.block_rows) - 1), 0).count;
+    const int t = (int)blockIdx.x, head = (int)blockIdx.y, h = head / a.group;
+    int b, count = 0, row = 0;
+    bool bad = false;
+    const KvSeq q = kv_seq_of_row(kb, c.page_size, t, &b, &bad);
+    Rows s = {};
+    if (b < kb.num_seqs && t >= q.r0) {
+        s = rows_of(kb, c.page_size, a, b);
+        const int nr = s.n * a.group;
+        row = (t - s.row0) * a.group + head - h * a.group;
+        const int r0 = row / pl.block_rows * pl.block_rows;
+        if (row < nr && nr >= pl.min_rows && nr <= pl.max_rows)
+            count = split_of(pl, range_of(a, s, r0, min(nr, r0 + pl.block_rows) - 1), 0).count;
+    }
     pdl_wait();
     if (count <= 1) return;
-    const float* src = part + part_index(pl, c, b, h, 0, row) * (D + 4);
-    join_row<D>(a, s, h, row, count, src, src, (int64_t)rows * (D + 4));
+    const float* src = part + part_index(kb, a, 0, t, head) * (D + 4);
+    join_row<D>(a, s, h, row, count, src, src, (int64_t)kb.rows * a.heads * (D + 4));
 }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -154,21 +160,23 @@ static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_
     return p;
 }
 
-// Chunks: 256 head rows a CTA (128 at D = 256); ranges only where the row blocks
-// leave SMs without work.
+// Chunks: 256 head rows a CTA (128 at D = 256), the grid as large as packed rows can
+// fill; ranges only where the row blocks leave SMs without work.
 static Plan chunk_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int min_rows) {
     Plan p = {};
-    const int64_t rows = (int64_t)a.max_rows * a.group;
     p.block_rows = c.D <= 128 ? 256 : 128;
-    p.row_blocks = (int)ceil_div(rows, p.block_rows);
-    p.min_rows = min_rows;
+    p.min_rows = min_rows > 1 ? min_rows : 1;
     p.max_rows = 0x7fffffff;
-    // row blocks with rows in them: max_rows may be one sequence's alone
-    int64_t blocks = (int64_t)b.num_seqs * p.row_blocks;
-    const int64_t packed = (int64_t)b.rows * a.group / p.block_rows + b.num_seqs;
-    if (blocks > packed) blocks = packed;
+    // every block but a sequence's last is full, and a sequence has min_rows at least
+    const int64_t rows = (int64_t)b.rows * a.group;
+    int64_t seqs = rows / p.min_rows;
+    if (seqs > b.num_seqs) seqs = b.num_seqs;
+    int64_t blocks = rows / p.block_rows + seqs;
+    const int64_t most = b.num_seqs * ceil_div((int64_t)a.max_rows * a.group, p.block_rows);
+    if (blocks > most) blocks = most;
+    p.row_blocks = (int)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
     const int64_t span = span_of(a, a.max_rows);
-    const int64_t n = kSizingSms / (blocks * c.heads);
+    const int64_t n = blocks > 0 ? kSizingSms / (blocks * c.heads) : 0;
     const int64_t q = n <= 1 ? span : ceil_div(span, n);
     set_splits(&p, span, q < 512 ? 512 : q);
     set_page(&p, c.page_size);
@@ -191,20 +199,19 @@ static Plans plans_of(const KvCache& c, const KvBatch& b, const KvAttn& a) {
     if (p.chunk) p.k = chunk_plan(c, b, a, p.few ? kFewRows + 1 : 0);
     return p;
 }
-static size_t part_bytes(const KvCache& c, const KvBatch& b, const Plan& p) {
+static size_t part_bytes(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p) {
     if (p.ctas > 0) return (size_t)p.ctas * 2 * p.block_rows * (c.D + 4) * sizeof(float);
     if (p.splits == 1) return 0;
-    return (size_t)b.num_seqs * c.heads * p.splits * p.row_blocks * p.block_rows * (c.D + 4) *
-           sizeof(float);
+    return (size_t)p.splits * b.rows * a.heads * (c.D + 4) * sizeof(float);
 }
 // Grids, and the few-rows kernel's line of units, fit 31 bits.
 static bool fits(const KvCache& c, const KvBatch& b, const Plan& p) {
     const int64_t items = (int64_t)b.num_seqs * p.row_blocks;
-    if (items * c.heads * p.block_rows > 0x7fffffffll) return false;
     if (p.ctas > 0)
-        return items * c.heads * ((int64_t)b.pages_per_seq * c.page_size / p.unit + 2) <=
-               0x7fffffffll;
-    return items * p.splits <= 0x7fffffffll;
+        return items <= 0x7fffffffll &&
+               items * c.heads * ((int64_t)b.pages_per_seq * c.page_size / p.unit + 2) <=
+                   0x7fffffffll;
+    return (int64_t)p.row_blocks * p.splits <= 0x7fffffffll;
 }
 
 template <int D>
@@ -214,9 +221,7 @@ static hbl_status combine_d(const KvCache& c, const KvBatch& b, const KvAttn& a,
         return launch_pdl(join_pieces_kernel<D>, 
                           dim3((unsigned)p.ctas, (unsigned)(p.max_rows < p.block_rows ? p.max_rows : p.block_rows)),
                           dim3(kThreads), 0, stream, c, b, a, p, part);
-    return launch_pdl(join_ranges_kernel<D>,
-                      dim3((unsigned)((int64_t)b.num_seqs * c.heads * p.row_blocks *
-                                      p.block_rows)),
+    return launch_pdl(join_ranges_kernel<D>, dim3((unsigned)b.rows, (unsigned)a.heads),
                       dim3(kThreads), 0, stream, c, b, a, p, part);
 }
 static hbl_status combine(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p,
@@ -234,7 +239,7 @@ static hbl_status combine(const KvCache& c, const KvBatch& b, const KvAttn& a, c
 
 size_t kv_attention_workspace(const KvCache& c, const KvBatch& b, const KvAttn& a) {
     const k12::Plans p = k12::plans_of(c, b, a);
-    return (p.few ? k12::part_bytes(c, b, p.f) : 0) + (p.chunk ? k12::part_bytes(c, b, p.k) : 0);
+    return (p.few ? k12::part_bytes(c, b, a, p.f) : 0) + (p.chunk ? k12::part_bytes(c, b, a, p.k) : 0);
 }
 
 hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn& a, void* ws,
@@ -254,7 +259,7 @@ hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn&
         if (st != HBL_OK) return st;
         st = k12::combine(c, b, a, p.k, part, stream);
         if (st != HBL_OK) return st;
-        part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + k12::part_bytes(c, b, p.k));
+        part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + k12::part_bytes(c, b, a, p.k));
     }
     if (p.few) {
         switch (c.D) {

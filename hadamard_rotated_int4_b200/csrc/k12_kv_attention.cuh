@@ -18,7 +18,7 @@ namespace k12 {
 // chunk_plan).
 struct Plan {
     int block_rows;          // head rows of a CTA
-    int row_blocks;          // blocks to a sequence's head rows
+    int row_blocks;          // few rows: most blocks to a sequence; chunks: most in all
     int min_rows, max_rows;  // the kernel takes sequences with so many head rows
     int splits;              // chunks: most ranges of positions of one row block
     int quantum;             // chunks: positions of a range (more where `splits` do not reach)
@@ -49,6 +49,11 @@ __device__ __forceinline__ Rows rows_of(const KvBatch& kb, int page_size, const 
     return r;
 }
 
+// First position that a window leaves visible from position p.
+__device__ __forceinline__ int window_begin(const KvAttn& a, int p) {
+    return a.window > 0 ? (int)max((int64_t)0, (int64_t)p - a.window + 1) : 0;
+}
+
 // Positions that head rows r0 .. r1 see between them (r0 == r1: that row's).
 struct Range {
     int begin, end;
@@ -57,8 +62,7 @@ __device__ __forceinline__ Range range_of(const KvAttn& a, const Rows& s, int r0
     Range w;
     w.end = a.causal ? min(s.len, s.first + r1 / a.group + 1) : s.len;
     w.end = max(w.end, 0);
-    w.begin = a.window > 0 ? max(0, s.first + r0 / a.group - a.window + 1) : 0;
-    w.begin = min(w.begin, w.end);
+    w.begin = min(window_begin(a, s.first + r0 / a.group), w.end);
     return w;
 }
 
@@ -78,11 +82,69 @@ __device__ __forceinline__ Split split_of(const Plan& pl, const Range& rg, int s
     return s;
 }
 
-// Partial results of chunks: [seq][cached head][split][row] x (D values, m, sum, 2 unused).
-__device__ __forceinline__ int64_t part_index(const Plan& pl, const KvCache& c, int b, int h,
-                                              int split, int row) {
-    return (((int64_t)b * c.heads + h) * pl.splits + split) * ((int64_t)pl.row_blocks *
-                                                               pl.block_rows) + row;
+// Partial results of chunks: [split][packed row][query head] x (D values, m, sum, 2 unused).
+__device__ __forceinline__ int64_t part_index(const KvBatch& kb, const KvAttn& a, int split,
+                                              int64_t t, int head) {
+    return ((int64_t)split * kb.rows + t) * a.heads + head;
+}
+
+// ---- chunks: which row block a CTA has
+// The row blocks of the sequences that the kernel takes, counted through: block
+// `index` is block rb of sequence b.  By all threads; b = -1 past the last block.
+struct Block {
+    int b, rb;
+};
+template <int kThreads>
+__device__ __forceinline__ Block block_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
+                                          const KvAttn& a, int index) {
+    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int found[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int before = 0;  // blocks of the sequences looked at
+    if (kb.num_seqs <= 8) {  // few: every thread for itself, without a barrier
+        for (int b = 0; b < kb.num_seqs; ++b) {
+            const int nr = rows_of(kb, c.page_size, a, b).n * a.group;
+            const int v = nr >= pl.min_rows && nr <= pl.max_rows
+                              ? (nr + pl.block_rows - 1) / pl.block_rows
+                              : 0;
+            if (index < before + v) return {b, index - before};
+            before += v;
+        }
+        return {-1, 0};
+    }
+    if (threadIdx.x == 0) found[0] = -1;
+    for (int i = 0; i < kb.num_seqs && before <= index; i += kThreads) {
+        const int b = i + (int)threadIdx.x;
+        int v = 0;
+        if (b < kb.num_seqs) {
+            const int nr = rows_of(kb, c.page_size, a, b).n * a.group;
+            if (nr >= pl.min_rows && nr <= pl.max_rows)
+                v = (nr + pl.block_rows - 1) / pl.block_rows;
+        }
+        int upto = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        __syncthreads();  // the sums of the step before are read
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) upto += warp_sum[w];
+            all += warp_sum[w];
+        }
+        upto += before;
+        if (index >= upto - v && index < upto) {
+            found[0] = b;
+            found[1] = index - (upto - v);
+        }
+        before += all;
+    }
+    __syncthreads();
+    return {found[0], found[1]};
 }
 
 // ---- few rows: all work in one line, cut into equal pieces

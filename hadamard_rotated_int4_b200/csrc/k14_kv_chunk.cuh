@@ -252,16 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     auto ofull = [&](int set) { return bar_s + 8u * (24 + set); };
     const uint32_t qfull = bar_s + 8u * 26, drain = bar_s + 8u * 27;
 
-    // ---- which rows, which positions: the longest row blocks start first
-    const int per_block = kb.num_seqs * pl.splits;
-    const int rb = pl.row_blocks - 1 - (int)(blockIdx.x / per_block);
-    const int b = (int)(blockIdx.x % per_block) / pl.splits;
-    const int split = (int)(blockIdx.x % per_block) % pl.splits, h = (int)blockIdx.y;
+    // ---- which rows, which positions: a sequence's last row blocks, the longest
+    // under a causal mask, start first
+    const int split = (int)(blockIdx.x % pl.splits), h = (int)blockIdx.y;
+    const k12::Block blk = k12::block_of<kThreads>(
+        pl, c, kb, a, pl.row_blocks - 1 - (int)(blockIdx.x / pl.splits));
+    if (blockIdx.x == 0 && h == 0)  // the descriptors, by the first CTA
+        for (int i = threadIdx.x; i < kb.num_seqs; i += kThreads)
+            if (k12::rows_of(kb, c.page_size, a, i).bad) report_status(status, HBL_ERR_INVALID_ARG);
+    if (blk.b < 0) return;
+    const int b = blk.b;
     const k12::Rows s = k12::rows_of(kb, c.page_size, a, b);
-    if (s.bad && split == 0 && rb == 0 && h == 0 && threadIdx.x == 0)
-        report_status(status, HBL_ERR_INVALID_ARG);
-    const int nr = s.n * a.group, row0 = rb * 128 * NQ;
-    if (nr < pl.min_rows || nr > pl.max_rows || row0 >= nr) return;
+    const int nr = s.n * a.group, row0 = blk.rb * 128 * NQ;
     const k12::Range rg = k12::range_of(a, s, row0, min(nr, row0 + 128 * NQ) - 1);
     const k12::Split sp = k12::split_of(pl, rg, split);
     if (split >= max(sp.count, 1)) return;
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 const int r = min(row0 + set * 128 + 32 * quarter + 8 * k + g, nr - 1);
                 const int p = s.first + r / a.group;
                 hi[k] = a.causal ? p + 1 : 0x7fffffff;
-                lo[k] = a.window > 0 ? p - a.window + 1 : 0;
+                lo[k] = k12::window_begin(a, p);
                 max_lo = max(max_lo, lo[k]);
                 min_hi = min(min_hi, hi[k]);
             }
@@ -543,7 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                         dst[n] = k12::row_out(a, s, h, row, M, L, there[n] && col == 0, &inv[n]) +
                                  col;
                     } else {
-                        float* to = part + k12::part_index(pl, c, b, h, split, row) * (D + 4);
+                        const int i = row / a.group;
+                        float* to = part + k12::part_index(kb, a, split, s.row0 + i,
+                                                           h * a.group + row - i * a.group) *
+                                               (D + 4);
                         if (there[n] && col == 0)
                             *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
                         dst[n] = to + col;
@@ -818,7 +823,7 @@ hbl_status launch(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Pl
                   int32_t* status, cudaStream_t stream) {
     auto kern = chunk_kernel<D, B>;
     if (!smem_attr_once(reinterpret_cast<const void*>(kern), Tile<D>::kSmem)) return HBL_ERR_CUDA;
-    const dim3 grid((unsigned)(kb.num_seqs * pl.row_blocks * pl.splits), (unsigned)c.heads);
+    const dim3 grid((unsigned)(pl.row_blocks * pl.splits), (unsigned)c.heads);
     kern<<<grid, kThreads, Tile<D>::kSmem, stream>>>(c, kb, a, pl, part, status);
     return cudaGetLastError() == cudaSuccess ? HBL_OK : HBL_ERR_CUDA;
 }

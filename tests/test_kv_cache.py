@@ -345,6 +345,34 @@ def test_attention_long_contexts(new, lens, bits):
 
 
 @gpu
+@pytest.mark.parametrize("rows,group", [(1, 1), (3, 8)])
+def test_attention_of_many_sequences(rows, group):
+    # more sequences than a CTA has threads, uneven and empty ones among them, so
+    # that the pieces of the common line begin and end anywhere
+    lens = [(37 * i) % 200 + (900 if i % 71 == 0 else 0) for i in range(700)]
+    new = [min(rows, n) if i % 5 else 0 for i, n in enumerate(lens)]
+    c = ref.Case(new, lens, heads=group, kv_heads=1, D=32, bits=4, page=16, seed=rows, extra_rows=2)
+    ref.check_attention(c, *attend(c, max_rows=rows))
+    # and one chunk among them
+    new[333], lens[333] = 150, 400
+    c = ref.Case(new, lens, heads=group, kv_heads=1, D=32, bits=4, page=16, seed=rows, extra_rows=2)
+    ref.check_attention(c, *attend(c, max_rows=150))
+
+
+@gpu
+def test_attention_under_a_wide_block_table():
+    # a table with room for 2^30 positions a sequence: the plan goes by its width, the
+    # work by the lengths
+    c = ref.Case([1, 2, 40, 1], [700, 90, 41, 3], heads=32, kv_heads=32, D=32, bits=2, page=16,
+                 wide=1 << 26)
+    ref.check_attention(c, *attend(c, max_rows=40))
+    c = ref.Case([1, 2, 1, 1], [700, 90, 41, 3], heads=32, kv_heads=32, D=32, bits=2, page=16,
+                 wide=1 << 26)
+    ref.check_attention(c, *attend(c, max_rows=2))
+    ref.check_attention(c, *attend(c, max_rows=2, window=0x7fffffff), window=0x7fffffff)
+
+
+@gpu
 @pytest.mark.parametrize("rows", [1, 6, 200])
 def test_attention_extreme_scores_scales_and_zero_rows(rows):
     c = ref.Case([rows], [260], heads=4, kv_heads=2, D=64, bits=4, seed=rows)
