@@ -90,61 +90,41 @@ __device__ __forceinline__ int64_t part_index(const KvBatch& kb, const KvAttn& a
 
 // ---- chunks: which row block a CTA has
 // The row blocks of the sequences that the kernel takes, counted through: block
-// `index` is block rb of sequence b.  By all threads; b = -1 past the last block.
+// `index` is block rb of sequence b, by one warp (b = -1 past the last block).  Up to
+// 32 sequences in layers, each one's last block, then each one's last but one;
+// more of them 32 at a time.
 struct Block {
     int b, rb;
 };
-template <int kThreads>
 __device__ __forceinline__ Block block_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
                                           const KvAttn& a, int index) {
-    __shared__ int warp_sum[kThreads / 32];
-    __shared__ int found[2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int before = 0;  // blocks of the sequences looked at
-    if (kb.num_seqs <= 8) {  // few: every thread for itself, without a barrier
-        for (int b = 0; b < kb.num_seqs; ++b) {
-            const int nr = rows_of(kb, c.page_size, a, b).n * a.group;
-            const int v = nr >= pl.min_rows && nr <= pl.max_rows
-                              ? (nr + pl.block_rows - 1) / pl.block_rows
-                              : 0;
-            if (index < before + v) return {b, index - before};
-            before += v;
-        }
-        return {-1, 0};
-    }
-    if (threadIdx.x == 0) found[0] = -1;
-    for (int i = 0; i < kb.num_seqs && before <= index; i += kThreads) {
-        const int b = i + (int)threadIdx.x;
-        int v = 0;
-        if (b < kb.num_seqs) {
-            const int nr = rows_of(kb, c.page_size, a, b).n * a.group;
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; i < kb.num_seqs; i += 32) {
+        int n = 0;  // row blocks of sequence i + lane
+        if (i + lane < kb.num_seqs) {
+            const int nr = rows_of(kb, c.page_size, a, i + lane).n * a.group;
             if (nr >= pl.min_rows && nr <= pl.max_rows)
-                v = (nr + pl.block_rows - 1) / pl.block_rows;
+                n = (nr + pl.block_rows - 1) / pl.block_rows;
         }
-        int upto = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
+        const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+        if (index < total) {
+            int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)n);
+            while (hi - lo > 1) {  // the layers before `lo` hold at most `index` blocks
+                const int mid = (lo + hi) / 2;
+                if ((int)__reduce_add_sync(0xffffffffu, (unsigned)min(n, mid)) <= index)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int left = index - (int)__reduce_add_sync(0xffffffffu, (unsigned)min(n, lo));
+            const uint32_t in = __ballot_sync(0xffffffffu, n > lo);
+            const bool mine = n > lo && __popc(in & ((1u << lane) - 1u)) == left;
+            const int who = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            return {i + who, __shfl_sync(0xffffffffu, n, who) - 1 - lo};
         }
-        __syncthreads();  // the sums of the step before are read
-        if (lane == 31) warp_sum[warp] = upto;
-        __syncthreads();
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) upto += warp_sum[w];
-            all += warp_sum[w];
-        }
-        upto += before;
-        if (index >= upto - v && index < upto) {
-            found[0] = b;
-            found[1] = index - (upto - v);
-        }
-        before += all;
+        index -= total;
     }
-    __syncthreads();
-    return {found[0], found[1]};
+    return {-1, 0};
 }
 
 // ---- few rows: all work in one line, cut into equal pieces

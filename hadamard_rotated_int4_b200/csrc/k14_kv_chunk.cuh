@@ -255,11 +255,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     // ---- which rows, which positions: a sequence's last row blocks, the longest
     // under a causal mask, start first
     const int split = (int)(blockIdx.x % pl.splits), h = (int)blockIdx.y;
-    const k12::Block blk = k12::block_of<kThreads>(
-        pl, c, kb, a, pl.row_blocks - 1 - (int)(blockIdx.x / pl.splits));
-    if (blockIdx.x == 0 && h == 0)  // the descriptors, by the first CTA
-        for (int i = threadIdx.x; i < kb.num_seqs; i += kThreads)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* const where = reinterpret_cast<int*>(bar_p);  // before the barriers are set up there
+    if (warp == 0) {
+        const k12::Block blk = k12::block_of(pl, c, kb, a, (int)(blockIdx.x / pl.splits));
+        if (lane == 0) {
+            where[0] = blk.b;
+            where[1] = blk.rb;
+        }
+    } else if (blockIdx.x == 0 && h == 0 && warp == 1) {  // the descriptors, by the first CTA
+        for (int i = lane; i < kb.num_seqs; i += 32)
             if (k12::rows_of(kb, c.page_size, a, i).bad) report_status(status, HBL_ERR_INVALID_ARG);
+    }
+    __syncthreads();
+    const k12::Block blk = {where[0], where[1]};
+    __syncthreads();
     if (blk.b < 0) return;
     const int b = blk.b;
     const k12::Rows s = k12::rows_of(kb, c.page_size, a, b);
@@ -272,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     const int tiles = (parts + T::kParts - 1) / T::kParts;
     const int sets = NQ == 2 && nr - row0 > 128 ? 2 : 1;  // row sets that have rows
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init_count(kfull(i), kConv);
