@@ -432,10 +432,15 @@ class KvCache:
     def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim):
         import torch
 
-        _dev(k_codes, torch.uint8, "k_codes")
-        _dev(v_codes, torch.uint8, "v_codes")
-        _dev(k_scales, torch.float32, "k_scales")
-        _dev(v_scales, torch.float32, "v_scales")
+        u8, f32 = torch.uint8, torch.float32
+        if not (k_codes.dtype is u8 and v_codes.dtype is u8 and k_scales.dtype is f32 and
+                v_scales.dtype is f32 and k_codes.is_cuda and k_codes.is_contiguous() and
+                v_codes.is_contiguous() and k_scales.is_contiguous() and
+                v_scales.is_contiguous()):
+            _dev(k_codes, u8, "k_codes")
+            _dev(v_codes, u8, "v_codes")
+            _dev(k_scales, f32, "k_scales")
+            _dev(v_scales, f32, "v_scales")
         shape, code_shape = k_scales.shape, k_codes.shape
         if len(shape) != 3 or len(code_shape) != 4 or code_shape[:3] != shape or \
                 v_codes.shape != code_shape or v_scales.shape != shape:
@@ -613,7 +618,8 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     q_row, q_head = _kv_rows(Q, cache, "Q")
     rows, heads, D = Q.shape
     if out is None:
-        out, o_row, o_head = Q.new_empty((rows, heads, D)), heads * D, D
+        out = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty((rows, heads, D))
+        o_row, o_head = heads * D, D
     else:
         o_row, o_head = _kv_rows(out, cache, "out", heads)
         if out.shape[0] != rows:

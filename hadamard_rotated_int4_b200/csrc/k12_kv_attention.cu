@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads) join_ranges_kernel(KvCache c, KvBatc
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSizingSms = 148;  // the workspace must not depend on the device
+// Row blocks that see at most this many positions are not split.
+constexpr int kWhole = 1024;
 // Sequences with at most this many head rows go to the few-rows kernel.
 constexpr int kFewRows = 32;
 
@@ -152,6 +154,16 @@ static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_
     const int64_t longest = (int64_t)b.pages_per_seq * c.page_size;
     const int64_t items = (int64_t)b.num_seqs * p.row_blocks * c.heads;
     p.unit = 64;
+    // where no block can see many positions, one unit holds them all: nothing is
+    // split, and nothing has to be joined
+    const int64_t seen = a.window > 0 && (int64_t)a.window + a.max_rows < longest
+                             ? (int64_t)a.window + a.max_rows
+                             : longest;
+    if (seen <= kWhole) {
+        p.unit = kWhole + 64;  // a block begins at a multiple of 64
+        p.min_units = 1;
+        p.whole = true;
+    }
     while (p.unit < (1 << 30) && items * (longest / p.unit + 2) > 0x7fffffffll) p.unit *= 2;
     // no more CTAs than the block table has room for pieces
     const int64_t most = ceil_div(items * (longest / p.unit + 2), p.min_units);
@@ -200,6 +212,7 @@ static Plans plans_of(const KvCache& c, const KvBatch& b, const KvAttn& a) {
     return p;
 }
 static size_t part_bytes(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p) {
+    if (p.whole) return 0;
     if (p.ctas > 0) return (size_t)p.ctas * 2 * p.block_rows * (c.D + 4) * sizeof(float);
     if (p.splits == 1) return 0;
     return (size_t)p.splits * b.rows * a.heads * (c.D + 4) * sizeof(float);
@@ -226,7 +239,7 @@ static hbl_status combine_d(const KvCache& c, const KvBatch& b, const KvAttn& a,
 }
 static hbl_status combine(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p,
                           float* part, cudaStream_t stream) {
-    if (p.ctas == 0 && p.splits == 1) return HBL_OK;
+    if (p.whole || (p.ctas == 0 && p.splits == 1)) return HBL_OK;
     switch (c.D) {
         case 32: return combine_d<32>(c, b, a, p, part, stream);
         case 64: return combine_d<64>(c, b, a, p, part, stream);

@@ -24,6 +24,7 @@ struct Plan {
     int quantum;             // chunks: positions of a range (more where `splits` do not reach)
     int ctas, min_units;     // few rows: CTAs, and the fewest units that are worth one
     int unit;                // few rows: positions of a unit, a multiple of 64
+    bool whole;              // few rows: a unit holds all that a block can see
     int seg_shift;           // 16, 32 or 64 positions (log2) that a page holds a multiple of
     uint32_t page_mul, page_shift;  // x / page_size = (mulhi(x, mul) + x) >> shift, x < 2^31
 
