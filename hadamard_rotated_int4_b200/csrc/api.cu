@@ -857,7 +857,7 @@ hbl_status hbl_kv_attention(const hbl_kv_cache* cache, const hbl_kv_batch* batch
     int sms = 0;
     st = device(&sms);
     if (st != HBL_OK) return st;
-    return launch_kv_attention(c, b, a, ws, dev_status, static_cast<cudaStream_t>(stream), sms);
+    return launch_kv_attention(c, b, a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 hbl_status hbl_expand_ternary(const uint32_t* W_packed, int N, int K, int8_t* W_s8,

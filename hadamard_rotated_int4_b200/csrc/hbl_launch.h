@@ -132,7 +132,7 @@ struct KvAttn {
 };
 size_t kv_attention_workspace(const KvCache& c, const KvBatch& b, const KvAttn& a);
 hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn& a, void* ws,
-                               int32_t* status, cudaStream_t stream, int num_sms);
+                               int32_t* status, cudaStream_t stream);
 
 // Self-test of the bounded-wait failure path (see k9_selftest.cu).
 hbl_status launch_bounded_wait_probe(int arrive, int timeout_us, int32_t* status,

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads) join_ranges_kernel(KvCache c, KvBatc
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kSizingSms = 148;  // the workspace must not depend on the device
+// SMs that the plans count on (the workspace must not depend on the device).
+constexpr int kSizingSms = 148;
 // Row blocks that see at most this many positions are not split.
 constexpr int kWhole = 1024;
 // Sequences with at most this many head rows go to the few-rows kernel.
@@ -231,9 +232,10 @@ template <int D>
 static hbl_status combine_d(const KvCache& c, const KvBatch& b, const KvAttn& a, const Plan& p,
                             float* part, cudaStream_t stream) {
     if (p.ctas > 0)
-        return launch_pdl(join_pieces_kernel<D>, 
-                          dim3((unsigned)p.ctas, (unsigned)(p.max_rows < p.block_rows ? p.max_rows : p.block_rows)),
-                          dim3(kThreads), 0, stream, c, b, a, p, part);
+        return launch_pdl(
+            join_pieces_kernel<D>,
+            dim3((unsigned)p.ctas, (unsigned)(p.max_rows < p.block_rows ? p.max_rows : p.block_rows)),
+            dim3(kThreads), 0, stream, c, b, a, p, part);
     return launch_pdl(join_ranges_kernel<D>, dim3((unsigned)b.rows, (unsigned)a.heads),
                       dim3(kThreads), 0, stream, c, b, a, p, part);
 }
@@ -256,8 +258,7 @@ size_t kv_attention_workspace(const KvCache& c, const KvBatch& b, const KvAttn& 
 }
 
 hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn& a, void* ws,
-                               int32_t* status, cudaStream_t stream, int num_sms) {
-    (void)num_sms;
+                               int32_t* status, cudaStream_t stream) {
     const k12::Plans p = k12::plans_of(c, b, a);
     if ((p.few && !k12::fits(c, b, p.f)) || (p.chunk && !k12::fits(c, b, p.k))) return HBL_ERR_SHAPE;
     float* part = static_cast<float*>(ws);

@@ -24,7 +24,7 @@ struct Plan {
     int quantum;             // chunks: positions of a range (more where `splits` do not reach)
     int ctas, min_units;     // few rows: CTAs, and the fewest units that are worth one
     int unit;                // few rows: positions of a unit, a multiple of 64
-    bool whole;              // few rows: a unit holds all that a block can see
+    bool whole;              // few rows: an item is one unit, whatever it sees
     int seg_shift;           // 16, 32 or 64 positions (log2) that a page holds a multiple of
     uint32_t page_mul, page_shift;  // x / page_size = (mulhi(x, mul) + x) >> shift, x < 2^31
 
@@ -149,7 +149,10 @@ __device__ __forceinline__ Item item_of(const Plan& pl, const KvCache& c, const 
         t.rg = range_of(a, t.s, r0, min(t.nr, r0 + pl.block_rows) - 1);
         t.from = t.rg.begin & ~63;
         // a block that sees nothing still has its rows stored
-        t.units = max(1, (int)((uint32_t)(t.rg.end - t.from + pl.unit - 1) / (uint32_t)pl.unit));
+        // (`whole`: one unit even of a sequence that breaks the caller's max_rows, whose
+        // rows then reach further back than was said: there is no room for pieces)
+        const uint32_t seen = (uint32_t)(t.rg.end - t.from), unit = (uint32_t)pl.unit;
+        t.units = pl.whole ? 1 : max(1, (int)((seen + unit - 1) / unit));
     }
     return t;
 }

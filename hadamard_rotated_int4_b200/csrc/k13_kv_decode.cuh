@@ -142,376 +142,371 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
     k12::Item im = k12::item_of(pl, c, kb, a, item);
     int before = line.before;  // the line's units before this item
     while (true) {
-    // ---- one head's part of an item: units [u0, u1) of im.units
-    while (at >= before + im.units * c.heads) {
-        before += im.units * c.heads;
-        im = k12::item_of(pl, c, kb, a, ++item);
-    }
-    const int b = item / pl.row_blocks, rb = item - b * pl.row_blocks;
-    const int h = (at - before) / im.units, u0 = (at - before) - h * im.units;
-    const int u1 = min(im.units, u0 + (stop - at));
-    at += u1 - u0;
-    const k12::Rows s = im.s;
-    const int nr = im.nr;
-    const int begin = im.from + u0 * pl.unit;
-    const int end = u1 == im.units ? im.rg.end : im.from + u1 * pl.unit;
+        // ---- one head's part of an item: units [u0, u1) of im.units
+        while (at >= before + im.units * c.heads) {
+            before += im.units * c.heads;
+            im = k12::item_of(pl, c, kb, a, ++item);
+        }
+        const int b = item / pl.row_blocks, rb = item - b * pl.row_blocks;
+        const int h = (at - before) / im.units, u0 = (at - before) - h * im.units;
+        const int u1 = min(im.units, u0 + (stop - at));
+        at += u1 - u0;
+        const k12::Rows s = im.s;
+        const int nr = im.nr;
+        const int begin = im.from + u0 * pl.unit;
+        const int end = u1 == im.units ? im.rg.end : im.from + u1 * pl.unit;
 
-    // per lane: the visible range of rows 2t, 2t + 1 of each tile
-    int lo[NT][2], hi[NT][2];
-    int all_lo = 0, all_hi = 0x7fffffff;  // every row sees [all_lo, all_hi)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = min(rb * R + 8 * n + 2 * t + e, nr - 1);
-            const k12::Range w = k12::range_of(a, s, r, r);
-            lo[n][e] = w.begin;
-            hi[n][e] = w.end;
-            all_lo = max(all_lo, w.begin);
-            all_hi = min(all_hi, w.end);
-        }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
-        all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
-    }
-
-    // ---- the ring of this warp
-    const int step = kWarps * KW;
-    const int first = begin + warp * KW;
-    const int steps = first < end ? (end - first + step - 1) / step : 0;
-    // one copy takes the positions of one page: seg of them, and a lane to each of
-    // K's and V's codes and scales (lane >> 2) of each segment (lane & 3)
-    const int seg_shift = min(pl.seg_shift, ilog2(KW)), seg = 1 << seg_shift;
-    const int my_seg = lane & 3, my_kind = lane >> 2;
-    const bool copies = my_kind < 4 && my_seg < (KW >> seg_shift);
-    auto page_of = [&](int it) {
-        const int key = first + it * step + (my_seg << seg_shift);
-        if (it >= steps || !copies || key >= end) return -2;  // nothing there
-        return kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
-    };
-    uint8_t* const my_base = my_kind == 0 ? c.kc : my_kind == 1 ? c.vc
-                             : reinterpret_cast<uint8_t*>(my_kind == 2 ? c.ks : c.vs);
-    const int my_row = my_kind < 2 ? St::kRow : 4;
-    const uint32_t my_dst = (my_kind < 2 ? my_kind * St::kCodes
-                                         : 2 * St::kCodes + (my_kind - 2) * St::kScales) +
-                            (my_seg << seg_shift) * my_row;
-    auto issue = [&](int it, int page) {
-        if (it >= steps) return;
-        const int slot = (done + it) % St::kCount;
-        const uint32_t st = ring + slot * St::kBytes, bar = bars + 8 * slot;
-        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-        if (page == -1) report_status(status, HBL_ERR_INVALID_ARG);
-        if (lane == 0) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * St::kCodes + 2 * St::kScales),
-                         "r"(there & 15u)
-                         : "memory");
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                         "r"((uint32_t)(__popc(there & 15u) * seg * (2 * St::kRow + 8)))
-                         : "memory");
-        }
-        __syncwarp();
-        if (page >= 0) {
-            const int key = first + it * step + (my_seg << seg_shift);
-            const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
-                                (key - (int)pl.div_page(key) * c.page_size);
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-                "[%3];" ::"r"(st + my_dst),
-                "l"(my_base + row * my_row), "r"((uint32_t)(seg * my_row)), "r"(bar)
-                : "memory");
-        }
-    };
-#pragma unroll
-    for (int it = 0; it < St::kCount; ++it) issue(it, page_of(it));
-    int next_page = page_of(St::kCount);
-
-    // ---- Q's fragments: pair p of lane t is codes (C w + i, C w + i + C/2), C = 2H
-    uint32_t q[NT][kPairs];
-    float xs[NT][2];  // scale * log2(e) of rows 2t, 2t + 1, and their power of two taken back
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = rb * R + 8 * n + g;
-        uint32_t raw[NK / 2];
-        const int i = r / a.group;
-        const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
-                              (int64_t)(h * a.group + (r - i * a.group)) * a.q_head + t * NK;
-#pragma unroll
-        for (int k = 0; k < NK / 8; ++k) {
-            const uint4 v = r < nr ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
-            raw[4 * k] = v.x;
-            raw[4 * k + 1] = v.y;
-            raw[4 * k + 2] = v.z;
-            raw[4 * k + 3] = v.w;
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int k = 0; k < NK / 2; ++k) {
-            const float2 f = bf16x2_to_f2(raw[k]);
-            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // 2^(14 - e), e the exponent of the row's largest value
-        const int e = max((int)(__float_as_uint(big) >> 23) - 127, -112);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        constexpr int C = NK < 2 * H ? NK : 2 * H;
-        static_for<0, kPairs>([&](auto pp) {
-            constexpr int p = decltype(pp)::value, w = p / (C / 2), i0 = p % (C / 2);
-            constexpr int e0 = C * w + i0, e1 = e0 + C / 2;
-            auto value = [&](int x) {
-                return __uint_as_float((x & 1) ? raw[x / 2] & 0xffff0000u : raw[x / 2] << 16);
-            };
-            q[n][p] = f2_to_f16x2(value(e0) * up, value(e1) * up);
-        });
-        // row 8n + g's lane holds e; lanes (., t) need rows 2t, 2t + 1
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int ee = __shfl_sync(0xffffffffu, e, (2 * t + u) * 4);
-            xs[n][u] = a.scale * 1.4426950408889634f * 0x1p-14f *
-                       __uint_as_float((uint32_t)(127 + ee) << 23);
-        }
-    }
-
-    float O[NV / 2][NT][4];
-    float m[NT][2], base[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int k = 0; k < NV / 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) O[k][n][e] = 0.f;
-        m[n][0] = m[n][1] = -CUDART_INF_F;
-        l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
-    }
-    const int kslot = (g >> 1) + 4 * (g & 1);  // this lane's K rows: kslot, kslot + 8
-
-    int it = 0;
-    for (; it < steps; ++it) {
-        const int ring_slot = (done + it) % St::kCount;
-        const uint32_t st = ring + ring_slot * St::kBytes;
-        if (!__all_sync(0xffffffffu, mbar_wait_clock(bars + 8 * ring_slot,
-                                                     ((done + it) / St::kCount) & 1, nullptr))) {
-            if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
-            break;
-        }
-        const int key0 = first + it * step;
-        const uint32_t flags = lds32(st + 2 * St::kCodes + 2 * St::kScales);
-        const bool plain = flags == (1u << (KW >> seg_shift)) - 1u && key0 >= all_lo &&
-                           key0 + KW <= min(all_hi, end);
-
-        // two blocks of 16 positions at a time: enough independent chains for three
-        // warps a scheduler, and half the code of the whole step (a CTA's first
-        // pass waits for its instructions)
-#pragma unroll 1
-        for (int sub = 0; sub < KW; sub += 16 * NB) {
-        float S[NB][NT][4];
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[blk][n][e] = 0.f;
-            const uint32_t r0 = st + (sub + 16 * blk + kslot) * St::kRow;
-            uint32_t w0[kKvWords<B, NK>], w1[kKvWords<B, NK>];
-            kv_lds_codes<B, NK>(r0, t, w0);
-            kv_lds_codes<B, NK>(r0 + 8 * St::kRow, t, w1);
-            if constexpr (NK < 2 * H) {  // 8 codes of 2 bits: one half word, split in two of 4
-                w0[0] = (w0[0] & 0xffu) | ((w0[0] & 0xff00u) << 8);
-                w1[0] = (w1[0] & 0xffu) | ((w1[0] & 0xff00u) << 8);
-            }
-            constexpr int P = NK < 2 * H ? NK / 2 : H;  // pairs of a word
-            static_for<0, kKvWords<B, NK>>([&](auto ww) {
-                constexpr int w = decltype(ww)::value;
-                uint32_t a0[P], a1[P];
-                kv_widen_f16<B, P>(w0[w], a0);
-                kv_widen_f16<B, P>(w1[w], a1);
-#pragma unroll
-                for (int p = 0; p < P; p += 2)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1], q[n][P * w + p],
-                                q[n][P * w + p + 1]);
-            });
-        }
-        // ---- exponents
-        float mx[NT][2], rsv[NB][2];  // rsv: 1 / sv of positions kslot, kslot + 8
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t sc = st + 2 * St::kCodes + 4 * (sub + 16 * blk + kslot + 8 * u);
-                const float sk = __uint_as_float(lds32(sc));
-                // a zero scale (an all-zero row: its codes are zero too) as 2^-100
-                const float lv = fmaxf(lg2(__uint_as_float(lds32(sc + St::kScales))), -100.f);
-                rsv[blk][u] = ex2(-lv);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        S[blk][n][2 * u + e] =
-                            __fmaf_rn(S[blk][n][2 * u + e], __fmul_rn(sk, xs[n][e]), lv);
-            }
-        if (!plain) {  // what is not visible becomes -inf, whatever is stored there
-#pragma unroll
-            for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int slot = sub + 16 * blk + kslot + 8 * u, key = key0 + slot;
-                    const bool there =
-                        ((flags >> (slot >> seg_shift)) & 1u) != 0 && key < end;
-                    if (!there) rsv[blk][u] = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (!(there && key >= lo[n][e] && key < hi[n][e]))
-                                S[blk][n][2 * u + e] = -CUDART_INF_F;
-                }
-        }
+        // per lane: the visible range of rows 2t, 2t + 1 of each tile
+        int lo[NT][2], hi[NT][2];
+        int all_lo = 0, all_hi = 0x7fffffff;  // every row sees [all_lo, all_hi)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[n][e] = fmaxf(S[0][n][e], S[0][n][2 + e]);
-#pragma unroll
-                for (int blk = 1; blk < NB; ++blk)
-                    mx[n][e] = max3(mx[n][e], S[blk][n][e], S[blk][n][2 + e]);
+                const int r = min(rb * R + 8 * n + 2 * t + e, nr - 1);
+                const k12::Range w = k12::range_of(a, s, r, r);
+                lo[n][e] = w.begin;
+                hi[n][e] = w.end;
+                all_lo = max(all_lo, w.begin);
+                all_hi = min(all_hi, w.end);
             }
-        // each lane looks at its own positions' largest; only when one is too far
-        // above the reference do the lanes of a row find their common one
-        bool far = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) far |= mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
-        if (__any_sync(0xffffffffu, far)) {
+        for (int o = 1; o < 4; o <<= 1) {
+            all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+            all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+        }
+
+        // ---- the ring of this warp
+        const int step = kWarps * KW;
+        const int first = begin + warp * KW;
+        const int steps = first < end ? (end - first + step - 1) / step : 0;
+        // one copy takes the positions of one page: seg of them, and a lane to each of
+        // K's and V's codes and scales (lane >> 2) of each segment (lane & 3)
+        const int seg_shift = min(pl.seg_shift, ilog2(KW)), seg = 1 << seg_shift;
+        const int my_seg = lane & 3, my_kind = lane >> 2;
+        const bool copies = my_kind < 4 && my_seg < (KW >> seg_shift);
+        auto page_of = [&](int it) {
+            const int key = first + it * step + (my_seg << seg_shift);
+            if (it >= steps || !copies || key >= end) return -2;  // nothing there
+            return kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
+        };
+        uint8_t* const my_base = my_kind == 0 ? c.kc : my_kind == 1 ? c.vc
+                                 : reinterpret_cast<uint8_t*>(my_kind == 2 ? c.ks : c.vs);
+        const int my_row = my_kind < 2 ? St::kRow : 4;
+        const uint32_t my_dst = (my_kind < 2 ? my_kind * St::kCodes
+                                             : 2 * St::kCodes + (my_kind - 2) * St::kScales) +
+                                (my_seg << seg_shift) * my_row;
+        auto issue = [&](int it, int page) {
+            if (it >= steps) return;
+            const int slot = (done + it) % St::kCount;
+            const uint32_t st = ring + slot * St::kBytes, bar = bars + 8 * slot;
+            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+            if (page == -1) report_status(status, HBL_ERR_INVALID_ARG);
+            if (lane == 0) {
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * St::kCodes + 2 * St::kScales),
+                             "r"(there & 15u)
+                             : "memory");
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                             "r"((uint32_t)(__popc(there & 15u) * seg * (2 * St::kRow + 8)))
+                             : "memory");
+            }
+            __syncwarp();
+            if (page >= 0) {
+                const int key = first + it * step + (my_seg << seg_shift);
+                const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
+                                    (key - (int)pl.div_page(key) * c.page_size);
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+                    "[%1], %2, [%3];" ::"r"(st + my_dst),
+                    "l"(my_base + row * my_row), "r"((uint32_t)(seg * my_row)), "r"(bar)
+                    : "memory");
+            }
+        };
+#pragma unroll
+        for (int it = 0; it < St::kCount; ++it) issue(it, page_of(it));
+        int next_page = page_of(St::kCount);
+
+        // ---- Q's fragments: pair p of lane t is codes (C w + i, C w + i + C/2), C = 2H
+        uint32_t q[NT][kPairs];
+        float xs[NT][2];  // scale * log2(e) of rows 2t, 2t + 1, and their power of two taken back
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = rb * R + 8 * n + g;
+            uint32_t raw[NK / 2];
+            const int i = r / a.group;
+            const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
+                                  (int64_t)(h * a.group + (r - i * a.group)) * a.q_head + t * NK;
+#pragma unroll
+            for (int k = 0; k < NK / 8; ++k) {
+                const uint4 v =
+                    r < nr ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
+                raw[4 * k] = v.x;
+                raw[4 * k + 1] = v.y;
+                raw[4 * k + 2] = v.z;
+                raw[4 * k + 3] = v.w;
+            }
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < NK / 2; ++k) {
+                const float2 f = bf16x2_to_f2(raw[k]);
+                big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^(14 - e), e the exponent of the row's largest value
+            const int e = max((int)(__float_as_uint(big) >> 23) - 127, -112);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            constexpr int C = NK < 2 * H ? NK : 2 * H;
+            static_for<0, kPairs>([&](auto pp) {
+                constexpr int p = decltype(pp)::value, w = p / (C / 2), i0 = p % (C / 2);
+                constexpr int e0 = C * w + i0, e1 = e0 + C / 2;
+                auto value = [&](int x) {
+                    return __uint_as_float((x & 1) ? raw[x / 2] & 0xffff0000u : raw[x / 2] << 16);
+                };
+                q[n][p] = f2_to_f16x2(value(e0) * up, value(e1) * up);
+            });
+            // row 8n + g's lane holds e; lanes (., t) need rows 2t, 2t + 1
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int ee = __shfl_sync(0xffffffffu, e, (2 * t + u) * 4);
+                xs[n][u] = a.scale * 1.4426950408889634f * 0x1p-14f *
+                           __uint_as_float((uint32_t)(127 + ee) << 23);
+            }
+        }
+
+        float O[NV / 2][NT][4];
+        float m[NT][2], base[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < NV / 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[k][n][e] = 0.f;
+            m[n][0] = m[n][1] = -CUDART_INF_F;
+            l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
+        }
+        const int kslot = (g >> 1) + 4 * (g & 1);  // this lane's K rows: kslot, kslot + 8
+
+        int it = 0;
+        for (; it < steps; ++it) {
+            const int use = done + it, ring_slot = use % St::kCount;
+            const uint32_t st = ring + ring_slot * St::kBytes;
+            if (!__all_sync(0xffffffffu, mbar_wait_clock(bars + 8 * ring_slot,
+                                                         (use / St::kCount) & 1, nullptr))) {
+                if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
+                break;
+            }
+            const int key0 = first + it * step;
+            const uint32_t flags = lds32(st + 2 * St::kCodes + 2 * St::kScales);
+            const bool plain = flags == (1u << (KW >> seg_shift)) - 1u && key0 >= all_lo &&
+                               key0 + KW <= min(all_hi, end);
+
+            float S[NB][NT][4];
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[blk][n][e] = 0.f;
+                const uint32_t r0 = st + (16 * blk + kslot) * St::kRow;
+                uint32_t w0[kKvWords<B, NK>], w1[kKvWords<B, NK>];
+                kv_lds_codes<B, NK>(r0, t, w0);
+                kv_lds_codes<B, NK>(r0 + 8 * St::kRow, t, w1);
+                if constexpr (NK < 2 * H) {  // 8 codes of 2 bits: one half word, split in two of 4
+                    w0[0] = (w0[0] & 0xffu) | ((w0[0] & 0xff00u) << 8);
+                    w1[0] = (w1[0] & 0xffu) | ((w1[0] & 0xff00u) << 8);
+                }
+                constexpr int P = NK < 2 * H ? NK / 2 : H;  // pairs of a word
+                static_for<0, kKvWords<B, NK>>([&](auto ww) {
+                    constexpr int w = decltype(ww)::value;
+                    uint32_t a0[P], a1[P];
+                    kv_widen_f16<B, P>(w0[w], a0);
+                    kv_widen_f16<B, P>(w1[w], a1);
+#pragma unroll
+                    for (int p = 0; p < P; p += 2)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1], q[n][P * w + p],
+                                    q[n][P * w + p + 1]);
+                });
+            }
+            // ---- exponents
+            float mx[NT][2], rsv[NB][2];  // rsv: 1 / sv of positions kslot, kslot + 8
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t sc = st + 2 * St::kCodes + 4 * (16 * blk + kslot + 8 * u);
+                    const float sk = __uint_as_float(lds32(sc));
+                    // a zero scale (an all-zero row: its codes are zero too) as 2^-100
+                    const float lv = fmaxf(lg2(__uint_as_float(lds32(sc + St::kScales))), -100.f);
+                    rsv[blk][u] = ex2(-lv);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            S[blk][n][2 * u + e] =
+                                __fmaf_rn(S[blk][n][2 * u + e], __fmul_rn(sk, xs[n][e]), lv);
+                }
+            if (!plain) {  // what is not visible becomes -inf, whatever is stored there
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int slot = 16 * blk + kslot + 8 * u, key = key0 + slot;
+                        const bool there =
+                            ((flags >> (slot >> seg_shift)) & 1u) != 0 && key < end;
+                        if (!there) rsv[blk][u] = 0.f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (!(there && key >= lo[n][e] && key < hi[n][e]))
+                                    S[blk][n][2 * u + e] = -CUDART_INF_F;
+                    }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    mx[n][e] = fmaxf(S[0][n][e], S[0][n][2 + e]);
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1)
-                        mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
-                    const float nm = fmaxf(m[n][e], mx[n][e]);
-                    const float f = nm == m[n][e] ? 1.f : ex2(m[n][e] - nm);
-                    m[n][e] = nm;
-                    // a row that has seen nothing: 2^(-inf) = 0 against any base
-                    base[n][e] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
-                    l[n][e] *= f;
-#pragma unroll
-                    for (int k = 0; k < NV / 2; ++k) {
-                        O[k][n][e] *= f;
-                        O[k][n][2 + e] *= f;
-                    }
+                    for (int blk = 1; blk < NB; ++blk)
+                        mx[n][e] = max3(mx[n][e], S[blk][n][e], S[blk][n][2 + e]);
                 }
-        }
-        // ---- weights and the second product
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-            uint32_t p[NT][2];
+            // each lane looks at its own positions' largest; only when one is too far
+            // above the reference do the lanes of a row find their common one
+            bool far = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+                far |= mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
+            if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float w[2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        w[e] = ex2(S[blk][n][2 * u + e] + base[n][e]);
-                        l[n][e] = __fmaf_rn(w[e], rsv[blk][u], l[n][e]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1)
+                            mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
+                        const float nm = fmaxf(m[n][e], mx[n][e]);
+                        const float f = nm == m[n][e] ? 1.f : ex2(m[n][e] - nm);
+                        m[n][e] = nm;
+                        // a row that has seen nothing: 2^(-inf) = 0 against any base
+                        base[n][e] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int k = 0; k < NV / 2; ++k) {
+                            O[k][n][e] *= f;
+                            O[k][n][2 + e] *= f;
+                        }
                     }
-                    p[n][u] = transpose8(f2_to_f16x2(w[0], w[1]));
-                }
-            const uint32_t r0 = st + St::kCodes + (sub + 16 * blk + t) * St::kRow;
-            constexpr int VW = kKvWords<B, NV>;
-            uint32_t v[4][VW];
+            }
+            // ---- weights and the second product
 #pragma unroll
-            for (int k = 0; k < 4; ++k) kv_lds_codes<B, NV>(r0 + 4 * k * St::kRow, g, v[k]);
-            constexpr int P = NV < H ? NV : H;  // values of a half word
-            static_for<0, NV / P>([&](auto hh) {
-                constexpr int hw = decltype(hh)::value, w = hw / 2;
-                constexpr uint32_t sel = hw & 1 ? 0x7632 : 0x5410;
-                uint32_t a0[P], a2[P];
-                kv_widen_f16<B, P>(__byte_perm(v[0][w], v[1][w], sel), a0);
-                kv_widen_f16<B, P>(__byte_perm(v[2][w], v[3][w], sel), a2);
+            for (int blk = 0; blk < NB; ++blk) {
+                uint32_t p[NT][2];
 #pragma unroll
-                for (int i = 0; i < P; i += 2)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(O[(P * hw + i) / 2][n], a0[i], a0[i + 1], a2[i], a2[i + 1],
-                                p[n][0], p[n][1]);
-            });
+                    for (int u = 0; u < 2; ++u) {
+                        float w[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            w[e] = ex2(S[blk][n][2 * u + e] + base[n][e]);
+                            l[n][e] = __fmaf_rn(w[e], rsv[blk][u], l[n][e]);
+                        }
+                        p[n][u] = transpose8(f2_to_f16x2(w[0], w[1]));
+                    }
+                const uint32_t r0 = st + St::kCodes + (16 * blk + t) * St::kRow;
+                constexpr int VW = kKvWords<B, NV>;
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) kv_lds_codes<B, NV>(r0 + 4 * k * St::kRow, g, v[k]);
+                constexpr int P = NV < H ? NV : H;  // values of a half word
+                static_for<0, NV / P>([&](auto hh) {
+                    constexpr int hw = decltype(hh)::value, w = hw / 2;
+                    constexpr uint32_t sel = hw & 1 ? 0x7632 : 0x5410;
+                    uint32_t a0[P], a2[P];
+                    kv_widen_f16<B, P>(__byte_perm(v[0][w], v[1][w], sel), a0);
+                    kv_widen_f16<B, P>(__byte_perm(v[2][w], v[3][w], sel), a2);
+#pragma unroll
+                    for (int i = 0; i < P; i += 2)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(O[(P * hw + i) / 2][n], a0[i], a0[i + 1], a2[i], a2[i + 1],
+                                    p[n][0], p[n][1]);
+                });
+            }
+            __syncwarp();  // the stage is read
+            issue(it + St::kCount, next_page);
+            next_page = page_of(it + St::kCount + 1);
         }
-        }
-        __syncwarp();  // the stage is read
-        issue(it + St::kCount, next_page);
-        next_page = page_of(it + St::kCount + 1);
-    }
-    // after a timeout: the copies still in flight, before their stages are reused
-    for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
-        mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
-                        nullptr);
-    done += steps;
-    const bool late = it < steps;
-    // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
+        // after a timeout: the copies still in flight, before their stages are reused
+        for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
+            mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
+                            nullptr);
+        done += steps;
+        const bool late = it < steps;
+        // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-    __syncthreads();  // the rings are free
-    float* so = reinterpret_cast<float*>(smem);         // [warp][R][D + 4]
-    float* sm = so + kWarps * R * (D + 4);              // [warp][R]: m, then l
-    float* sl = sm + kWarps * R;
+                for (int o = 4; o < 32; o <<= 1)
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+        __syncthreads();  // the rings are free
+        float* so = reinterpret_cast<float*>(smem);         // [warp][R][D + 4]
+        float* sm = so + kWarps * R * (D + 4);              // [warp][R]: m, then l
+        float* sl = sm + kWarps * R;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 8 * n + 2 * t + e;
-            float* dst = so + (warp * R + r) * (D + 4) + g * NV;
-            if constexpr (NV >= 4) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * n + 2 * t + e;
+                float* dst = so + (warp * R + r) * (D + 4) + g * NV;
 #pragma unroll
                 for (int k = 0; k < NV / 4; ++k)
                     reinterpret_cast<float4*>(dst)[k] =
                         make_float4(O[2 * k][n][e], O[2 * k][n][2 + e], O[2 * k + 1][n][e],
                                     O[2 * k + 1][n][2 + e]);
+                if (g == 0) {
+                    sm[warp * R + r] = m[n][e];
+                    sl[warp * R + r] = l[n][e];
+                }
             }
-            if (g == 0) {
-                sm[warp * R + r] = m[n][e];
-                sl[warp * R + r] = l[n][e];
+        __syncthreads();
+        constexpr int kPer = D / 4;  // threads of a row, four values each
+        for (int x = threadIdx.x; x < R * kPer; x += kThreads) {
+            const int r = x / kPer, d = (x % kPer) * 4, row = rb * R + r;
+            if (row >= nr) break;
+            float M = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * R + r]);
+            float L = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = sm[w * R + r];
+                const float f = mw == -CUDART_INF_F ? 0.f : ex2(mw - M);
+                const float4 v = *reinterpret_cast<const float4*>(so + (w * R + r) * (D + 4) + d);
+                L = __fmaf_rn(sl[w * R + r], f, L);
+                y.x = __fmaf_rn(v.x, f, y.x);
+                y.y = __fmaf_rn(v.y, f, y.y);
+                y.z = __fmaf_rn(v.z, f, y.z);
+                y.w = __fmaf_rn(v.w, f, y.w);
+            }
+            if (u0 == 0 && u1 == im.units) {
+                k12::store_row4(a, s, h, row, d, y, M - kShift, L);
+            } else {
+                float* dst = k12::slot_of(part, pl, D, blockIdx.x, u0 == 0) + r * (D + 4);
+                *reinterpret_cast<float4*>(dst + d) = y;
+                if (d == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M - kShift, L);
             }
         }
-    __syncthreads();
-    constexpr int kPer = D / 4;  // threads of a row, four values each
-    for (int x = threadIdx.x; x < R * kPer; x += kThreads) {
-        const int r = x / kPer, d = (x % kPer) * 4, row = rb * R + r;
-        if (row >= nr) break;
-        float M = -CUDART_INF_F;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * R + r]);
-        float L = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = sm[w * R + r];
-            const float f = mw == -CUDART_INF_F ? 0.f : ex2(mw - M);
-            const float4 v = *reinterpret_cast<const float4*>(so + (w * R + r) * (D + 4) + d);
-            L = __fmaf_rn(sl[w * R + r], f, L);
-            y.x = __fmaf_rn(v.x, f, y.x);
-            y.y = __fmaf_rn(v.y, f, y.y);
-            y.z = __fmaf_rn(v.z, f, y.z);
-            y.w = __fmaf_rn(v.w, f, y.w);
-        }
-        if (u0 == 0 && u1 == im.units) {
-            k12::store_row4(a, s, h, row, d, y, M - kShift, L);
-        } else {
-            float* dst = k12::slot_of(part, pl, D, blockIdx.x, u0 == 0) + r * (D + 4);
-            *reinterpret_cast<float4*>(dst + d) = y;
-            if (d == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M - kShift, L);
-        }
-    }
-    // the rings' memory goes back to the copies; a CTA that has lost one ends here
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (__syncthreads_or(late) || at >= stop) return;
+        // the rings' memory goes back to the copies; a CTA that has lost one ends here
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (__syncthreads_or(late) || at >= stop) return;
     }
 }
 
@@ -526,8 +521,8 @@ hbl_status launch(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Pl
 }
 
 template <int D>
-hbl_status launch_d(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Plan& pl, float* part,
-                    int32_t* status, cudaStream_t stream) {
+hbl_status launch_d(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Plan& pl,
+                    float* part, int32_t* status, cudaStream_t stream) {
     auto by_nt = [&](auto bits) -> hbl_status {
         constexpr int B = decltype(bits)::value;
         if constexpr (D <= 128) {

@@ -452,6 +452,24 @@ def test_rows_past_max_rows_are_left_out_and_reported():
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_past_max_rows_under_a_wide_window(D):
+    # 2000 rows where 2 were announced: those two, far back, see nearly the whole
+    # sequence, which the plan (a window of 40 rows) made no room to split
+    c = ref.Case([2000, 1], [2010, 30], heads=4, kv_heads=2, D=D, bits=4, seed=D)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert hbl.kv_attention_workspace_size(c.rows, 4, c.cache, 2, c.table.shape[1], max_rows=2,
+                                           causal=False, window=40) == 0
+    O, lse = attend(c, causal=False, window=40, max_rows=2, status=st)
+    assert st.item() == 1
+    want, z, tol, tol_z = ref.attention(c, causal=False, window=40)
+    for r in (0, 1, 2000):
+        assert bool(((O[r].double() - want[r]).abs() <= tol[r]).all())
+        assert bool(((lse[r].double() - z[r]).abs() <= tol_z[r]).all())
+    assert bool((O[2:2000] == 7).all())
+
+
+@gpu
 def test_offsets_past_32_bits():
     # a pool of over 2^31 bytes of codes whose last pages are used
     pages, heads, page, D = 18000, 8, 64, 256
