@@ -225,7 +225,7 @@ static bool fits(const KvCache& c, const KvBatch& b, const Plan& p) {
         return items <= 0x7fffffffll &&
                items * c.heads * ((int64_t)b.pages_per_seq * c.page_size / p.unit + 2) <=
                    0x7fffffffll;
-    return (int64_t)p.row_blocks * p.splits <= 0x7fffffffll;
+    return (int64_t)p.row_blocks * p.splits * c.heads <= 0x7fffffffll;
 }
 
 template <int D>

@@ -90,38 +90,62 @@ __device__ __forceinline__ int64_t part_index(const KvBatch& kb, const KvAttn& a
 }
 
 // ---- chunks: which row block a CTA has
-// The row blocks of the sequences that the kernel takes, counted through: block
-// `index` is block rb of sequence b, by one warp (b = -1 past the last block).  Up to
-// 32 sequences in layers, each one's last block, then each one's last but one;
-// more of them 32 at a time.
+// The row blocks (of BLOCK head rows) of the sequences that the kernel takes, in the
+// order that their CTAs start: of each 32 sequences the block that ends farthest back
+// first, which under a causal mask is the one with the most to do, so that short ones
+// fill the gaps at the end.  Block `index` is block rb of sequence b (b = -1: there
+// are not so many); by one warp, a lane to a sequence.
 struct Block {
     int b, rb;
 };
+template <int BLOCK>
 __device__ __forceinline__ Block block_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
                                           const KvAttn& a, int index) {
+    auto sum = [](int v) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)v); };
     const int lane = threadIdx.x & 31;
     for (int i = 0; i < kb.num_seqs; i += 32) {
-        int n = 0;  // row blocks of sequence i + lane
+        Rows s = {};
+        int n = 0, tokens = 0;  // row blocks of sequence i + lane, and its last token
         if (i + lane < kb.num_seqs) {
-            const int nr = rows_of(kb, c.page_size, a, i + lane).n * a.group;
-            if (nr >= pl.min_rows && nr <= pl.max_rows)
-                n = (nr + pl.block_rows - 1) / pl.block_rows;
+            s = rows_of(kb, c.page_size, a, i + lane);
+            const int nr = s.n * a.group;
+            if (nr >= pl.min_rows && nr <= pl.max_rows) {
+                n = (nr + BLOCK - 1) / BLOCK;
+                tokens = s.n - 1;
+            }
         }
-        const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+        const int total = sum(n);
         if (index < total) {
-            int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)n);
-            while (hi - lo > 1) {  // the layers before `lo` hold at most `index` blocks
-                const int mid = (lo + hi) / 2;
-                if ((int)__reduce_add_sync(0xffffffffu, (unsigned)min(n, mid)) <= index)
+            // this lane's blocks that end at position `end` or behind it
+            auto count = [&](int end) {
+                if (!a.causal) return s.len >= end ? n : 0;
+                const int64_t x = (int64_t)end - s.first - 1;  // the block has token x
+                if (end <= 0 || x <= 0) return n;
+                return x > tokens ? 0 : n - (int)x * a.group / BLOCK;
+            };
+            int lo = 0, hi = (int)__reduce_max_sync(
+                            0xffffffffu, (unsigned)(n == 0 ? 0 : a.causal ? max(s.first + s.n, 0)
+                                                                          : s.len)) + 1;
+            while (hi - lo > 1) {  // more than `index` end at lo or behind, not at hi
+                const int mid = lo + (hi - lo) / 2;
+                if (sum(count(mid)) > index)
                     lo = mid;
                 else
                     hi = mid;
             }
-            const int left = index - (int)__reduce_add_sync(0xffffffffu, (unsigned)min(n, lo));
-            const uint32_t in = __ballot_sync(0xffffffffu, n > lo);
-            const bool mine = n > lo && __popc(in & ((1u << lane) - 1u)) == left;
-            const int who = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-            return {i + who, __shfl_sync(0xffffffffu, n, who) - 1 - lo};
+            // those that end at lo, sequence by sequence
+            const int past = count(lo + 1), mine = count(lo) - past;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const int left = index - sum(past);
+            const bool here = left < upto && left >= upto - mine;
+            const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            const int rb = n - past - 1 - (left - (upto - mine));
+            return {i + who, __shfl_sync(0xffffffffu, rb, who)};
         }
         index -= total;
     }

@@ -252,18 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     auto ofull = [&](int set) { return bar_s + 8u * (24 + set); };
     const uint32_t qfull = bar_s + 8u * 26, drain = bar_s + 8u * 27;
 
-    // ---- which rows, which positions: a sequence's last row blocks, the longest
-    // under a causal mask, start first
-    const int split = (int)(blockIdx.x % pl.splits), h = (int)blockIdx.y;
+    // ---- which rows, which positions: all heads of one block, then those of the next
+    const int split = (int)(blockIdx.x % pl.splits), nth = (int)(blockIdx.x / pl.splits);
+    const int h = nth % c.heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* const where = reinterpret_cast<int*>(bar_p);  // before the barriers are set up there
     if (warp == 0) {
-        const k12::Block blk = k12::block_of(pl, c, kb, a, (int)(blockIdx.x / pl.splits));
+        const k12::Block blk = k12::block_of<128 * NQ>(pl, c, kb, a, nth / c.heads);
         if (lane == 0) {
             where[0] = blk.b;
             where[1] = blk.rb;
         }
-    } else if (blockIdx.x == 0 && h == 0 && warp == 1) {  // the descriptors, by the first CTA
+    } else if (blockIdx.x == 0 && warp == 1) {  // the descriptors, by the first CTA
         for (int i = lane; i < kb.num_seqs; i += 32)
             if (k12::rows_of(kb, c.page_size, a, i).bad) report_status(status, HBL_ERR_INVALID_ARG);
     }
@@ -508,12 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 tmem_st_16x128b_x8(s_t, p[0]);
                 tmem_st_16x128b_x8(s_t + (16u << 16), p[1]);
                 tmem_wait_st();
-                // The last scores are issued before the one but last product, so that
-                // product may still be outstanding here; a parity tells neighbouring
-                // phases apart only, so it is waited for before the last product can be
-                // issued, and the wait behind the loop is for one phase.
-                if (i > 0 && i + 1 == parts) ok = wait.all(ofull(set), (i - 1) & 1);
-                if (!ok) break;
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -522,20 +516,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                         mbar_arrive_one(scempty(j % kScaleStages));
                 }
             }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float z = l[r].x + l[r].y;
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                l[r].x = z;
+            }
             // ---- the accumulator out, 32 columns at a time through this warp's own
-            // part of the queries' tile (its rows' queries are used up: the last
-            // product has landed)
-            if (ok && parts > 0) ok = wait.all(ofull(set), (parts - 1) & 1);
+            // part of the queries' tile (they are used up).  Every product has landed with
+            // the drain's single phase (a set's last product alone could not be told
+            // from the one before the one before it by a parity).
+            if (ok && parts > 0) ok = wait.all(drain, 0);
             if (ok) {
                 tmem_fence_after();
                 float* stage = reinterpret_cast<float*>(smem_base + (qbase - base_s)) + quarter * 512;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float z = l[r].x + l[r].y;
-                    z += __shfl_xor_sync(0xffffffffu, z, 1);
-                    z += __shfl_xor_sync(0xffffffffu, z, 2);
-                    l[r].x = z;
-                }
                 // this lane's rows on the way out, 16 hf + 4 i + lane / 8, and its four columns
                 constexpr int N = 8;
                 const int col = (lane & 7) * 4;
@@ -668,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             // ================= widening
             const int cw = warp - kConvWarp0;
             const Lane<D> ln(lane);
-            uint32_t raw[T::kMine][B];
+            uint32_t raw[2][T::kMine][B];  // keys, values: loaded a tile ahead
             int page[2][T::kMine];  // of the units that are loaded next: keys, values
             // this warp's i-th unit of a tile of K (values: V's are dealt out from
             // another warp on, so that all get about the same)
@@ -682,8 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                                          ? kv_page(kb, c.num_pages, b, (int)pl.div_page(key))
                                          : -1;
             };
-            // the codes of a unit, whose page was looked up two phases ago
+            // the codes of a unit, whose page was looked up a tile ago
             auto load = [&](int phase, int i) {
+                uint32_t(&to)[B] = raw[phase & 1][i];
                 const int key = key_of(phase, i), pg = page[phase & 1][i];
                 if (pg >= 0) {
                     const int64_t row = ((int64_t)pg * c.heads + h) * c.page_size +
@@ -694,23 +690,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
 #pragma unroll
                         for (int k = 0; k < B / 4; ++k) {
                             const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
-                            raw[i][4 * k] = v.x;
-                            raw[i][4 * k + 1] = v.y;
-                            raw[i][4 * k + 2] = v.z;
-                            raw[i][4 * k + 3] = v.w;
+                            to[4 * k] = v.x;
+                            to[4 * k + 1] = v.y;
+                            to[4 * k + 2] = v.z;
+                            to[4 * k + 3] = v.w;
                         }
                     } else if constexpr (B == 2) {
                         const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-                        raw[i][0] = v.x;
-                        raw[i][1] = v.y;
+                        to[0] = v.x;
+                        to[1] = v.y;
                     } else {
 #pragma unroll
                         for (int k = 0; k < B; ++k)
-                            raw[i][k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+                            to[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
                     }
                 } else {  // nothing there: any finite codes (their weight is zero)
 #pragma unroll
-                    for (int k = 0; k < B; ++k) raw[i][k] = 0;
+                    for (int k = 0; k < B; ++k) to[k] = 0;
                 }
                 load_page(phase + 2, i);
             };
@@ -719,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             for (int k = 0; k < 4; ++k) lane_at[k] = chunk_at(KT, ln.row, ln.group, k);
             auto store = [&](auto bf16, int i, int u, uint32_t dst) {
                 uint32_t out[16];
-                widen32<B, decltype(bf16)::value>(raw[i], out);
+                widen32<B, decltype(bf16)::value>(raw[decltype(bf16)::value ? 0 : 1][i], out);
                 // (row & 7, which the swizzle goes by, is the lane's own where a unit
                 // has a multiple of eight rows, and flips bit 2 in odd units of four)
                 const uint32_t to = dst + u * Lane<D>::kRows * 128;
@@ -730,24 +726,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                            make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
             };
             const float xscale = a.scale * 1.4426950408889634f;
-            // scales of a tile: four positions a lane, by the last widening warp
+            // scales of a tile: four positions a lane, by the last widening warp, which
+            // looks up their page a tile before
             float4 sk, sv;
             bool sc_there = false;
+            int sc_page = -2;
+            auto load_scales_page = [&](int j) {
+                const int key = sp.begin + j * KT + 4 * lane;
+                if (4 * lane < KT && key < sp.end) {
+                    sc_page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
+                } else {
+                    sc_page = -2;  // no position; -1: no such page
+                }
+            };
             auto load_scales = [&](int j) {
                 const int key = sp.begin + j * KT + 4 * lane;
-                sc_there = false;
-                if (4 * lane < KT && key < sp.end) {
-                    const int page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
-                    if (page >= 0) {
-                        const int64_t row = ((int64_t)page * c.heads + h) * c.page_size +
-                                            (key - (int)pl.div_page(key) * c.page_size);
-                        sk = *reinterpret_cast<const float4*>(c.ks + row);
-                        sv = *reinterpret_cast<const float4*>(c.vs + row);
-                        sc_there = true;
-                    } else {
-                        report_status(status, HBL_ERR_INVALID_ARG);
-                    }
+                sc_there = sc_page >= 0;
+                if (sc_page == -1) report_status(status, HBL_ERR_INVALID_ARG);
+                if (sc_there) {
+                    const int64_t row = ((int64_t)sc_page * c.heads + h) * c.page_size +
+                                        (key - (int)pl.div_page(key) * c.page_size);
+                    sk = *reinterpret_cast<const float4*>(c.ks + row);
+                    sv = *reinterpret_cast<const float4*>(c.vs + row);
                 }
+                load_scales_page(j + 1);
             };
             auto store_scales = [&](int j) {
                 if (4 * lane >= KT) return;
@@ -770,7 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 sts128(sc + KT * 8 + lane * 16, make_uint4(f(rs[0]), f(rs[1]), f(rs[2]), f(rs[3])));
             };
             const bool scales = cw == kConv - 1;
-            if (scales) load_scales(0);
+            if (scales) {
+                load_scales_page(0);
+                load_scales(0);
+            }
 #pragma unroll
             for (int i = 0; i < T::kMine; ++i) {
                 load_page(0, i);
@@ -778,6 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             }
 #pragma unroll
             for (int i = 0; i < T::kMine; ++i) load(0, i);
+#pragma unroll
+            for (int i = 0; i < T::kMine; ++i) load(1, i);
             bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < tiles && ok; ++j) {
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     store_scales(j);
                     __syncwarp();
                     if (lane == 0) mbar_arrive_one(scfull(j % kScaleStages));
-                    if (j + 1 < tiles) load_scales(j + 1);
+                    load_scales(j + 1);
                 }
                 if (j >= 2) ok = wait.all(kempty(st), par);
                 if (!ok) break;
@@ -798,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 for (int i = 0; i < T::kMine; ++i) {
                     const int u = unit(false, i);
                     if (u < T::kUnits) store(ic_bool<true>{}, i, u, k_s + st * T::kStage);
-                    load(2 * j + 1, i);
+                    load(2 * j + 2, i);
                 }
                 fence_async();
                 __syncwarp();
@@ -809,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 for (int i = 0; i < T::kMine; ++i) {
                     const int u = unit(true, i);
                     if (u < T::kUnits) store(ic_bool<false>{}, i, u, v_s + st * T::kStage);
-                    if (j + 1 < tiles) load(2 * j + 2, i);
+                    load(2 * j + 3, i);
                 }
                 fence_async();
                 __syncwarp();
@@ -832,7 +839,7 @@ hbl_status launch(const KvCache& c, const KvBatch& kb, const KvAttn& a, const Pl
                   int32_t* status, cudaStream_t stream) {
     auto kern = chunk_kernel<D, B>;
     if (!smem_attr_once(reinterpret_cast<const void*>(kern), Tile<D>::kSmem)) return HBL_ERR_CUDA;
-    const dim3 grid((unsigned)(pl.row_blocks * pl.splits), (unsigned)c.heads);
+    const unsigned grid = (unsigned)(pl.row_blocks * pl.splits * c.heads);  // (it fits 31 bits)
     kern<<<grid, kThreads, Tile<D>::kSmem, stream>>>(c, kb, a, pl, part, status);
     return cudaGetLastError() == cudaSuccess ? HBL_OK : HBL_ERR_CUDA;
 }
