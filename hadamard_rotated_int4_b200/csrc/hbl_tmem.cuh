@@ -27,6 +27,22 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t a, float (&r)[32]) {
                  : "r"(a));
 }
 
+// 32x32b: thread i of a warp holds columns 0..31 of lane i of its quarter.
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t a, float (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+                 "}, [%32];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]),
+                   "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]),
+                   "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]),
+                   "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
+                   "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+                   "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]),
+                   "=f"(r[30]), "=f"(r[31])
+                 : "r"(a));
+}
+
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t a, float (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
                  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"

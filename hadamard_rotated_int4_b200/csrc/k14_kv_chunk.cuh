@@ -47,8 +47,7 @@ namespace k14 {
 using k12::Plan;
 
 constexpr int kThreads = 512;
-constexpr int kConv = 7;             // widening warps
-constexpr int kConvWarp0 = 8, kMmaWarp = 15;
+constexpr int kMmaWarp = 15;
 constexpr float kShift = 6.f;        // weights are held times 2^6 ...
 constexpr float kLazy = 8.f;         // ... and may pass the reference by 2^8
 constexpr int kScaleStages = 4;
@@ -65,6 +64,7 @@ struct Tile {
     static constexpr int kScale = KT * 12;               // (ck, ck, lv, lv) a pair, then 1/sv
     static constexpr int kBars = 256;
     static constexpr int kUnits = KT * (D / 32) / 32;    // warp units of 32 x 32 codes
+    static constexpr int kConv = 15 - 4 * NQ;            // widening warps
     static constexpr int kMine = (kUnits + kConv - 1) / kConv;
     static constexpr int kSmem = kQ + 4 * kStage + kScaleStages * kScale + kBars + 1024;
 };
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init_count(kfull(i), kConv);
+            mbar_init_count(kfull(i), T::kConv);
             mbar_init_count(kempty(i), 1);
-            mbar_init_count(vfull(i), kConv);
+            mbar_init_count(vfull(i), T::kConv);
             mbar_init_count(vempty(i), 1);
             mbar_init_count(ofull(i), 1);
         }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, status};
 
-    if (warp < kConvWarp0) {
+    if (warp < 4 * NQ) {
         // ================= softmax
         reg_alloc<144>();
         const int set = warp >> 2, quarter = warp & 3, g = lane >> 2, t = lane & 3;
@@ -324,12 +324,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             const Lane<D> ql(lane);
             const uint32_t qbase = q_s + set * 128 * T::kPanels * 128;
             constexpr int kUnits = 128 / Lane<D>::kRows;
-            // (two units' loads in flight)
+            constexpr int kLoads = kUnits >= 16 ? 4 : kUnits / 4;  // units in flight
 #pragma unroll 1
-            for (int u0 = quarter; u0 < kUnits; u0 += 8) {
-                uint32_t raw[2][16];
+            for (int u0 = quarter; u0 < kUnits; u0 += 4 * kLoads) {
+                uint32_t raw[kLoads][16];
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
+                for (int v = 0; v < kLoads; ++v) {
                     const int u = u0 + 4 * v, row = u * Lane<D>::kRows + ql.row;
                     const int r = row0 + set * 128 + row, i = r / a.group;
                     const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                                           ql.group * 32;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint4 z = u < kUnits && r < nr
+                        const uint4 z = r < nr
                                             ? reinterpret_cast<const uint4*>(src)[k]
                                             : make_uint4(0, 0, 0, 0);
                         raw[v][4 * k] = z.x;
@@ -347,9 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     }
                 }
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
+                for (int v = 0; v < kLoads; ++v) {
                     const int u = u0 + 4 * v;
-                    if (u >= kUnits) break;
                     uint32_t out[16];
                     static_for<0, 16>([&](auto pp) {
                         constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
@@ -523,87 +522,98 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 z += __shfl_xor_sync(0xffffffffu, z, 2);
                 l[r].x = z;
             }
-            // ---- the accumulator out, 32 columns at a time through this warp's own
-            // part of the queries' tile (they are used up).  Every product has landed with
-            // the drain's single phase (a set's last product alone could not be told
-            // from the one before the one before it by a parity).
+            // ---- the accumulator out, a lane to a row, 32 columns at a time.  Every product
+            // has landed with the drain's single phase (a set's last product alone could not
+            // be told from the one before the one before it by a parity).
             if (ok && parts > 0) ok = wait.all(drain, 0);
             if (ok) {
                 tmem_fence_after();
-                float* stage = reinterpret_cast<float*>(smem_base + (qbase - base_s)) + quarter * 512;
-                // this lane's rows on the way out, 16 hf + 4 i + lane / 8, and its four columns
-                constexpr int N = 8;
-                const int col = (lane & 7) * 4;
-                void* dst[N];
-                float inv[N];
-                bool there[N];
+                // row 8k + g's sum and reference sit in lane 4g
+                float L = 0.f, M = 0.f;
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    // row 8k + g's sums sit in lane 4g
-                    const int k = n >> 1, from = (4 * (n & 1) + (lane >> 3)) * 4;
-                    const float L = __shfl_sync(0xffffffffu, l[k].x, from);
-                    const float M = __shfl_sync(0xffffffffu, m[k], from) - kShift;
-                    const int row = row0 + set * 128 + 32 * quarter + 4 * n + (lane >> 3);
-                    there[n] = row < nr;
-                    if (sp.count <= 1) {
-                        dst[n] = k12::row_out(a, s, h, row, M, L, there[n] && col == 0, &inv[n]) +
-                                 col;
-                    } else {
-                        const int i = row / a.group;
-                        float* to = part + k12::part_index(kb, a, split, s.row0 + i,
-                                                           h * a.group + row - i * a.group) *
-                                               (D + 4);
-                        if (there[n] && col == 0)
-                            *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
-                        dst[n] = to + col;
-                        inv[n] = 1.f;
+                for (int k = 0; k < 4; ++k) {
+                    const float lk = __shfl_sync(0xffffffffu, l[k].x, 4 * (lane & 7));
+                    const float mk = __shfl_sync(0xffffffffu, m[k], 4 * (lane & 7));
+                    if (lane >> 3 == k) {
+                        L = lk;
+                        M = mk - kShift;
                     }
                 }
-#pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc)
+                const int row = row0 + set * 128 + 32 * quarter + lane;
+                const bool there = row < nr, whole = sp.count <= 1;
+                float inv = 1.f;
+                uint8_t* dst;
+                if (whole) {
+                    dst = reinterpret_cast<uint8_t*>(
+                        k12::row_out(a, s, h, row, M, L, there, &inv));
+                } else {
+                    const int i = row / a.group;
+                    float* to = part + k12::part_index(kb, a, split, s.row0 + i,
+                                                       h * a.group + row - i * a.group) *
+                                           (D + 4);
+                    if (there) *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
+                    dst = reinterpret_cast<uint8_t*>(to);
+                }
+                // Two neighbouring lanes store 32 bytes of one's row, then of the other's:
+                // whole sectors.  even and odd: those rows, from this lane's 16 bytes on.
+                const bool is_odd = lane & 1;
+                const uint64_t mine = reinterpret_cast<uint64_t>(dst);
+                const uint64_t next = __shfl_xor_sync(0xffffffffu, mine, 1);
+                const bool next_there = __shfl_xor_sync(0xffffffffu, (int)there, 1) != 0;
+                uint8_t* const even =
+                    reinterpret_cast<uint8_t*>(is_odd ? next : mine) + 16 * (lane & 1);
+                uint8_t* const odd =
+                    reinterpret_cast<uint8_t*>(is_odd ? mine : next) + 16 * (lane & 1);
+                const bool even_there = is_odd ? next_there : there;
+                const bool odd_there = is_odd ? there : next_there;
+                auto store_pair = [&](const uint32_t* lo, const uint32_t* hi, int at) {
+                    uint32_t e[4], o[4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float o[16];
-                        if (parts > 0) {
-                            tmem_ld_16x256b_x4(o_t + ((uint32_t)(16 * hf) << 16) + 32 * cc, o);
-                            tmem_wait_ld(o);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = 0.f;
-                        }
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int rr = 8 * u + g;  // of these 16 rows
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    // column 8k + 2t + e holds this value of the 32
-                                    const int n = 8 * k + 2 * t + e;
-                                    const int d = place_of<B>(n);
-                                    stage[rr * 32 + (d ^ ((rr & 7) * 4))] = o[4 * k + 2 * u + e];
-                                }
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int rr = 4 * i + (lane >> 3), n = 4 * hf + i;
-                            const float4 y = *reinterpret_cast<const float4*>(
-                                stage + rr * 32 + (col ^ ((rr & 7) * 4)));
-                            if (!there[n]) continue;
-                            if (sp.count <= 1)
-                                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst[n]) + 32 * cc) =
-                                    make_uint2(f2_to_bf16x2(y.x * inv[n], y.y * inv[n]),
-                                               f2_to_bf16x2(y.z * inv[n], y.w * inv[n]));
-                            else
-                                *reinterpret_cast<float4*>(static_cast<float*>(dst[n]) + 32 * cc) = y;
-                        }
-                        __syncwarp();
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t got =
+                            __shfl_xor_sync(0xffffffffu, is_odd ? lo[k] : hi[k], 1);
+                        e[k] = is_odd ? got : lo[k];
+                        o[k] = is_odd ? hi[k] : got;
                     }
+                    if (even_there)
+                        *reinterpret_cast<uint4*>(even + at) = make_uint4(e[0], e[1], e[2], e[3]);
+                    if (odd_there)
+                        *reinterpret_cast<uint4*>(odd + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                };
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    float o[32];
+                    if (parts > 0) {
+                        tmem_ld_32x32b_x32(o_t + 32 * cc, o);
+                        tmem_wait_ld(o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    float y[32];  // back in the order of D
+                    static_for<0, 32>([&](auto n) {
+                        y[place_of<B>(decltype(n)::value)] = o[decltype(n)::value] * inv;
+                    });
+                    if (whole) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = f2_to_bf16x2(y[2 * e], y[2 * e + 1]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            store_pair(w + 8 * q, w + 8 * q + 4, 64 * cc + 32 * q);
+                    } else {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(y[e]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            store_pair(w + 8 * q, w + 8 * q + 4, 128 * cc + 32 * q);
+                    }
+                }
             }
         }
     } else {
-        reg_dealloc<112>();
+        if (warp >= 8) reg_dealloc<112>();  // (warps 4 .. 7 keep what they have)
         if (warp == kMmaWarp) {
             // ================= MMA issue
             if (parts > 0) {
@@ -661,13 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             }
         } else if (tiles > 0) {
             // ================= widening
-            const int cw = warp - kConvWarp0;
+            const int cw = warp >= 8 ? warp - 8 : warp + 3;  // warps 8 .. 14, then 4 .. 7
             const Lane<D> ln(lane);
             uint32_t raw[2][T::kMine][B];  // keys, values: loaded a tile ahead
             int page[2][T::kMine];  // of the units that are loaded next: keys, values
-            // this warp's i-th unit of a tile of K (values: V's are dealt out from
-            // another warp on, so that all get about the same)
-            auto unit = [&](bool val, int i) { return (val ? (cw + 5) % kConv : cw) + kConv * i; };
+            // this warp's i-th unit of a tile of K (values: dealt out from where the keys'
+            // left off, so that all get about the same)
+            constexpr int kConv = T::kConv, kTurn = kConv - T::kUnits % kConv;
+            auto unit = [&](bool val, int i) { return (val ? (cw + kTurn) % kConv : cw) + kConv * i; };
             auto key_of = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
                 return sp.begin + (phase >> 1) * KT + unit(phase & 1, i) * Lane<D>::kRows + ln.row;
             };
