@@ -104,28 +104,29 @@ __device__ __forceinline__ Block block_of(const Plan& pl, const KvCache& c, cons
     auto sum = [](int v) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)v); };
     const int lane = threadIdx.x & 31;
     for (int i = 0; i < kb.num_seqs; i += 32) {
-        Rows s = {};
-        int n = 0, tokens = 0;  // row blocks of sequence i + lane, and its last token
+        // of sequence i + lane: its row blocks, the position of its first token and how
+        // many follow it (without a causal mask all blocks end with the sequence)
+        int n = 0, first = -1, tokens = 0;
         if (i + lane < kb.num_seqs) {
-            s = rows_of(kb, c.page_size, a, i + lane);
+            const Rows s = rows_of(kb, c.page_size, a, i + lane);
             const int nr = s.n * a.group;
             if (nr >= pl.min_rows && nr <= pl.max_rows) {
                 n = (nr + BLOCK - 1) / BLOCK;
-                tokens = s.n - 1;
+                first = a.causal ? s.first : s.len - 1;
+                tokens = a.causal ? s.n - 1 : 0;
             }
         }
         const int total = sum(n);
         if (index < total) {
-            // this lane's blocks that end at position `end` or behind it
+            // this lane's blocks that end at position `end` or behind it: those from the
+            // block of token x on
             auto count = [&](int end) {
-                if (!a.causal) return s.len >= end ? n : 0;
-                const int64_t x = (int64_t)end - s.first - 1;  // the block has token x
-                if (end <= 0 || x <= 0) return n;
-                return x > tokens ? 0 : n - (int)x * a.group / BLOCK;
+                const unsigned x = (unsigned)(end - 1) - (unsigned)first;
+                const int from = (int)(x * (unsigned)a.group / BLOCK);
+                return end <= 0 || end - 1 < first ? n : x > (unsigned)tokens ? 0 : n - from;
             };
-            int lo = 0, hi = (int)__reduce_max_sync(
-                            0xffffffffu, (unsigned)(n == 0 ? 0 : a.causal ? max(s.first + s.n, 0)
-                                                                          : s.len)) + 1;
+            int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu,
+                                                    (unsigned)max(first + tokens + 1, 0)) + 1;
             while (hi - lo > 1) {  // more than `index` end at lo or behind, not at hi
                 const int mid = lo + (hi - lo) / 2;
                 if (sum(count(mid)) > index)

@@ -256,62 +256,66 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     const int split = (int)(blockIdx.x % pl.splits), nth = (int)(blockIdx.x / pl.splits);
     const int h = nth % c.heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* const where = reinterpret_cast<int*>(bar_p);  // before the barriers are set up there
+    int* const where = reinterpret_cast<int*>(bar_p + 248);
     if (warp == 0) {
         const k12::Block blk = k12::block_of<128 * NQ>(pl, c, kb, a, nth / c.heads);
         if (lane == 0) {
             where[0] = blk.b;
             where[1] = blk.rb;
         }
-    } else if (blockIdx.x == 0 && warp == 1) {  // the descriptors, by the first CTA
-        for (int i = lane; i < kb.num_seqs; i += 32)
-            if (k12::rows_of(kb, c.page_size, a, i).bad) report_status(status, HBL_ERR_INVALID_ARG);
-    }
-    __syncthreads();
-    const k12::Block blk = {where[0], where[1]};
-    __syncthreads();
-    if (blk.b < 0) return;
-    const int b = blk.b;
-    const k12::Rows s = k12::rows_of(kb, c.page_size, a, b);
-    const int nr = s.n * a.group, row0 = blk.rb * 128 * NQ;
-    const k12::Range rg = k12::range_of(a, s, row0, min(nr, row0 + 128 * NQ) - 1);
-    const k12::Split sp = k12::split_of(pl, rg, split);
-    if (split >= max(sp.count, 1)) return;
-    pdl_launch_dependents();
-    const int parts = sp.count == 0 ? 0 : (sp.end - sp.begin + 63) / 64;
-    const int tiles = (parts + T::kParts - 1) / T::kParts;
-    const int sets = NQ == 2 && nr - row0 > 128 ? 2 : 1;  // row sets that have rows
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init_count(kfull(i), T::kConv);
-            mbar_init_count(kempty(i), 1);
-            mbar_init_count(vfull(i), T::kConv);
-            mbar_init_count(vempty(i), 1);
-            mbar_init_count(ofull(i), 1);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init_count(kfull(i), T::kConv);
+                mbar_init_count(kempty(i), 1);
+                mbar_init_count(vfull(i), T::kConv);
+                mbar_init_count(vempty(i), 1);
+                mbar_init_count(ofull(i), 1);
+            }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init_count(sfull(i), 1);
+                mbar_init_count(pfull(i), 4);
+            }
+            for (int i = 0; i < kScaleStages; ++i) {
+                mbar_init_count(scfull(i), 1);
+                mbar_init_count(scempty(i), 4 * NQ);
+            }
+            mbar_init_count(qfull, 4 * NQ);
+            mbar_init_count(drain, 1);
+            *abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init_count(sfull(i), 1);
-            mbar_init_count(pfull(i), 4);
-        }
-        for (int i = 0; i < kScaleStages; ++i) {
-            mbar_init_count(scfull(i), 1);
-            mbar_init_count(scempty(i), 4 * sets);
-        }
-        mbar_init_count(qfull, 4 * sets);
-        mbar_init_count(drain, 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_fence_before();
+    } else if (blockIdx.x == 0 && warp == 2) {  // the descriptors, by the first CTA
+        for (int i = lane; i < kb.num_seqs; i += 32)
+            if (k12::rows_of(kb, c.page_size, a, i).bad) report_status(status, HBL_ERR_INVALID_ARG);
     }
-    tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    const int b = where[0], rb = where[1];
+    k12::Rows s = {};
+    k12::Split sp = {};
+    const int row0 = rb * 128 * NQ;
+    int nr = 0;
+    if (b >= 0) {
+        s = k12::rows_of(kb, c.page_size, a, b);
+        nr = s.n * a.group;
+        sp = k12::split_of(pl, k12::range_of(a, s, row0, min(nr, row0 + 128 * NQ) - 1), split);
+    }
+    const bool work = b >= 0 && split < max(sp.count, 1);
+    if (work) pdl_launch_dependents();
+    const int parts = !work || sp.count == 0 ? 0 : (sp.end - sp.begin + 63) / 64;
+    const int tiles = (parts + T::kParts - 1) / T::kParts;
+    // row sets that have rows; what they all report is reported twice where one is missing
+    const int sets = !work ? 0 : NQ == 2 && nr - row0 > 128 ? 2 : 1;
+    auto arrive_for_all = [&](uint32_t bar) {
+        for (int k = sets; k <= NQ; ++k) mbar_arrive_one(bar);
+    };
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, status};
 
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive_one(qfull);
+            if (lane == 0) arrive_for_all(qfull);
 
             // ---- rows of this thread: 16 hf + 8 u + g of the warp's 32
             int lo[4], hi[4];
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 if (lane == 0) {
                     mbar_arrive_one(pfull(sb));
                     if (i % T::kParts == T::kParts - 1 || i + 1 == parts)
-                        mbar_arrive_one(scempty(j % kScaleStages));
+                        arrive_for_all(scempty(j % kScaleStages));
                 }
             }
 #pragma unroll
