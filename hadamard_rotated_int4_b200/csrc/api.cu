@@ -728,7 +728,8 @@ static hbl_status check_kv_shape(const hbl_kv_cache* c, const hbl_kv_batch* b) {
     if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > 65536) return HBL_ERR_SHAPE;
     if (b->num_seqs < 0 || b->pages_per_seq < 0 || b->rows < 0) return HBL_ERR_SHAPE;
     // positions are 32-bit
-    if ((int64_t)b->pages_per_seq * c->page_size > 0x7fffffffll) return HBL_ERR_SHAPE;
+    // (the kernels step a little past the last position in 32 bits)
+    if ((int64_t)b->pages_per_seq * c->page_size > 0x7fffffffll - 4095) return HBL_ERR_SHAPE;
     return HBL_OK;
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

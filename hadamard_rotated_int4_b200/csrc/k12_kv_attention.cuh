@@ -77,9 +77,9 @@ __device__ __forceinline__ Split split_of(const Plan& pl, const Range& rg, int s
     Split s;
     const int from = rg.begin & ~63, total = rg.end > rg.begin ? rg.end - from : 0;
     const int q = max(pl.quantum, ((total + pl.splits - 1) / pl.splits + 127) & ~127);
-    s.count = (total + q - 1) / q;
-    s.begin = from + split * q;
-    s.end = min(s.begin + q, rg.end);
+    s.count = (int)(((uint32_t)total + (uint32_t)q - 1u) / (uint32_t)q);
+    s.begin = (int)((uint32_t)from + (uint32_t)split * (uint32_t)q);
+    s.end = (int)min((int64_t)s.begin + q, (int64_t)rg.end);
     return s;
 }
 

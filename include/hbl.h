@@ -338,7 +338,7 @@ HBL_API hbl_status hbl_kv_quant(const uint16_t* X, int64_t rows, int D, int bits
  * Position p of sequence b is slot p % page_size of page
  * block_table[b][p / page_size].  head_dim D in {32, 64, 128, 256}; bits in
  * {2, 3, 4, 8}; page_size a multiple of 16 in [16, 65536]; 1 <= num_kv_heads
- * <= 65535; pages_per_seq * page_size < 2^31. */
+ * <= 65535; pages_per_seq * page_size <= 2^31 - 4096. */
 typedef struct {
     uint8_t* k_codes;
     float* k_scales;

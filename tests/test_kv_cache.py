@@ -57,7 +57,8 @@ SHARED = [(dict(bits=5), 1), (dict(bits=0), 1), (dict(head_dim=96), 2), (dict(he
           (dict(num_pages=0), 2), (dict(num_kv_heads=0), 2), (dict(num_kv_heads=1 << 16, num_heads=1 << 16), 2),
           (dict(page_size=8), 2), (dict(page_size=24), 2), (dict(page_size=1 << 17), 2),
           (dict(num_seqs=-1), 2), (dict(pages_per_seq=-1), 2), (dict(rows=-1), 2),
-          (dict(pages_per_seq=1 << 27), 2), (dict(k_codes=None), 1), (dict(v_scales=None), 1),
+          (dict(pages_per_seq=1 << 27), 2), (dict(pages_per_seq=(1 << 27) - 255), 2),
+          (dict(k_codes=None), 1), (dict(v_scales=None), 1),
           (dict(cu_seqlens=None), 1), (dict(block_table=None), 1), (dict(v_codes=A + 8), 3),
           (dict(k_scales=A + 4), 3), (dict(kv_lens=A + 2), 3), (dict(rows=0), 0),
           (dict(num_seqs=0), 0)]
