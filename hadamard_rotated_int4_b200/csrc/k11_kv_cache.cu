@@ -14,7 +14,7 @@
 // head rows (K heads, then V heads; D/16 lanes a row, 16 values a lane): the
 // token's sequence, position and page are found once per warp, by one round of
 // loads and a ballot per 32 sequences instead of a chain of dependent loads.
-#include "hbl_kv.cuh"
+#include "hbl_kv_codes.cuh"
 
 namespace hbl {
 namespace k11 {
@@ -30,6 +30,12 @@ struct Task {
     int per_task;       // head rows of one task
     int64_t tasks;
 };
+
+// A task's token; by a division of 32 bits where they do, a tenth of the instructions.
+__device__ __forceinline__ int row_of(const Task& k, int64_t task) {
+    if (k.tasks <= 0xffffffffll) return (int)((uint32_t)task / (uint32_t)k.tasks_per_row);
+    return (int)(task / k.tasks_per_row);
+}
 
 // Where the token of this warp's task stands in the cache.
 struct Place {
@@ -80,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas) write_kernel(KvCache c, 
     const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
     for (int64_t task = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; task < k.tasks;
          task += warps) {
-        const int t = (int)(task / k.tasks_per_row);
+        const int t = row_of(k, task);
         const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
         const int last = min(first + k.per_task, 2 * c.heads);
         uint4 raw[kSteps][2];
@@ -110,14 +116,35 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas) write_kernel(KvCache c, 
     check_batch(c, kb, status);
 }
 
-// value = (u - 2^(B-1)) * scale, one fp32 rounding, then one to bf16.
+// value = (u - 2^(B-1)) * scale, one fp32 rounding, then one to bf16.  The codes
+// become fp16 pairs first, which hold them exactly: about one instruction a code,
+// where taking each out of its bits and converting it takes three.
 template <int B>
 __device__ __forceinline__ void values16(const KvHalf<B> (&h)[2], float scale, float (&v)[16]) {
-    constexpr int kMask = (1 << B) - 1, kHalf = 1 << (B - 1);
+    constexpr int H = kKvHalfCodes<B>, W = 16 / (2 * H);
+    uint32_t w[W];
+    if constexpr (B == 8) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int u = (int)(h[i / 8] >> (B * (i % 8))) & kMask;
-        v[i] = __fmul_rn((float)(u - kHalf), scale);
+        for (int i = 0; i < W; ++i) w[i] = (uint32_t)(h[i / 2] >> (32 * (i % 2)));
+    } else if constexpr (B == 4) {
+        w[0] = h[0];
+        w[1] = h[1];
+    } else if constexpr (B == 3) {
+        w[0] = kv_spread3(h[0]);
+        w[1] = kv_spread3(h[1]);
+    } else {
+        w[0] = h[0] | (h[1] << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        uint32_t pair[H];
+        kv_widen_f16<B, H>(w[i], pair);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            const float2 f = __half22float2(reinterpret_cast<const __half2&>(pair[k]));
+            v[2 * H * i + k] = __fmul_rn(f.x, scale);
+            v[2 * H * i + k + H] = __fmul_rn(f.y, scale);
+        }
     }
 }
 
@@ -131,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) read_kernel(KvCache c, Kv
     const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
     for (int64_t task = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; task < k.tasks;
          task += warps) {
-        const int t = (int)(task / k.tasks_per_row);
+        const int t = row_of(k, task);
         const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
         const int last = min(first + k.per_task, 2 * c.heads);
         const Place p = place_of(c, kb, t, status);
