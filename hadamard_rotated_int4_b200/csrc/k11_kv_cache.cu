@@ -90,13 +90,15 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas) write_kernel(KvCache c, 
         const int first = (int)(task - (int64_t)t * k.tasks_per_row) * k.per_task;
         const int last = min(first + k.per_task, 2 * c.heads);
         uint4 raw[kSteps][2];
+        const uint16_t* const k0 = x.k + (int64_t)t * x.k_row + li * kKvVpl;
+        const uint16_t* const v0 =
+            x.v + (int64_t)t * x.v_row - (int64_t)c.heads * x.v_head + li * kKvVpl;
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {  // the rows load while their place is found
             const int r = first + step * RPW + sub;  // K heads, then V heads
             const bool isv = r >= c.heads;
-            const uint16_t* src = isv ? x.v + (int64_t)t * x.v_row + (int64_t)(r - c.heads) * x.v_head
-                                      : x.k + (int64_t)t * x.k_row + (int64_t)r * x.k_head;
-            const uint4* s = reinterpret_cast<const uint4*>(src + li * kKvVpl);
+            const uint4* s = reinterpret_cast<const uint4*>((isv ? v0 : k0) +
+                                                            r * (isv ? x.v_head : x.k_head));
             raw[step][0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
             raw[step][1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
         }
