@@ -115,9 +115,14 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // SMs that the plans count on (the workspace must not depend on the device).
 constexpr int kSizingSms = 148;
-// Row blocks that see at most this many positions are not split.
+// Row blocks that see at most this many positions are not split.  Not splitting saves
+// a launch (22 -> 17 us a call, host included), and on the GPU, 8 cached heads of 128
+// at 4 bits, one sequence of 517: 9.5 against 11.4 us split, 8 of 1000: 11.5 / 14.0,
+// 256 of 400: 43 / 71; one of 1000 takes 11.0 / 8.5, 64 of 1000: 30.9 / 29.4.
 constexpr int kWhole = 1024;
-// Sequences with at most this many head rows go to the few-rows kernel.
+// Sequences with at most this many head rows go to the few-rows kernel.  16 sequences
+// of 4000, 4 query heads to each of 8 cached ones: 32 head rows take 61 us there and
+// 87.5 us in chunks, 48 take 83.5 and 87.9, 64 take 101.5 and 88.3.
 constexpr int kFewRows = 32;
 
 // Round-up reciprocal of the page size: exact for x < 2^31.
@@ -141,8 +146,9 @@ static void set_splits(Plan* p, int64_t span, int64_t quantum) {
     p->quantum = (int)(q < 0x40000000 ? q : 0x40000000);
 }
 
-// Few rows: blocks of 8 or 16 head rows; as many CTAs as run at once, so that all
-// work is one wave of equal pieces.
+// Few rows: blocks of 8 head rows, or 16 where there are more than 8 (16 sequences of
+// 4000 with 16 head rows each: 42 us, in blocks of 8 46.5; with 32: 61 and 76); as
+// many CTAs as run at once, so that all work is one wave of equal pieces.
 static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_t rows) {
     Plan p = {};
     p.block_rows = c.D <= 128 && rows > 8 ? 16 : 8;
@@ -150,6 +156,7 @@ static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_
     p.min_rows = 0;
     p.max_rows = (int)rows;
     p.ctas = kSizingSms * (p.block_rows == 8 && c.D <= 128 ? 3 : 2);
+    // (one sequence of 2000: 9.3 us, 12.4 with pieces of one unit, 12.9 with sixteen)
     p.min_units = 4;
     // the whole line stays below 2^31 units
     const int64_t longest = (int64_t)b.pages_per_seq * c.page_size;
@@ -174,7 +181,8 @@ static Plan few_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int64_
 }
 
 // Chunks: 256 head rows a CTA (128 at D = 256), the grid as large as packed rows can
-// fill; ranges only where the row blocks leave SMs without work.
+// fill; ranges only where the row blocks leave SMs without work, of 256 positions at
+// least (64 rows of one sequence of 4000: 27.3 us; 32.3 with 512, 44.2 with 1024).
 static Plan chunk_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int min_rows) {
     Plan p = {};
     p.block_rows = c.D <= 128 ? 256 : 128;
@@ -191,7 +199,7 @@ static Plan chunk_plan(const KvCache& c, const KvBatch& b, const KvAttn& a, int 
     const int64_t span = span_of(a, a.max_rows);
     const int64_t n = blocks > 0 ? kSizingSms / (blocks * c.heads) : 0;
     const int64_t q = n <= 1 ? span : ceil_div(span, n);
-    set_splits(&p, span, q < 512 ? 512 : q);
+    set_splits(&p, span, q < 256 ? 256 : q);
     set_page(&p, c.page_size);
     return p;
 }

@@ -24,12 +24,21 @@
 // subnormal fp16, with the offset taken off the sums, save the fma, but the
 // tensor cores align such products by their exponent field and lose ten bits.)
 //
-// One CTA: one sequence, cached head, block of 8*NT rows (query heads of the
-// sequence's new tokens) and a range of positions; its warps take KW positions
-// in turn, each through a ring of bulk copies of its own (no CTA barrier in
-// the loop), and join their (m, sum, O) in shared memory.  Ranges of one
-// sequence are joined by the combine kernel.  The reference point m follows the
-// running maximum only when a score passes it by more than 2^8.
+// One CTA: an equal piece of the line of all work (k12_kv_attention.cuh): one after
+// the other, parts of one sequence, cached head and block of 8*NT rows (query heads
+// of the sequence's new tokens).  Its warps take KW positions in turn, each through a
+// ring of bulk copies of its own (no CTA barrier in the loop), and join their
+// (m, sum, O) in shared memory.  What pieces share of one head is joined by the next
+// kernel.  The reference point m follows the running maximum only when a score
+// passes it by more than 2^8.
+//
+// Measured, graph replay, D = 128, 32 query heads over 8: 64 sequences of 1024 to
+// 8192 on the 4-bit cache 76 us (44 to read it once), two of 131071 on the 3-bit one
+// 73 us (33); five rows of each of 16 sequences, 8-bit, 32 heads of 64, 68 us (44).
+// Loads alone take 60 and 43 us in the first two, all but the widening 63 and 54.
+// Tried and slower: four CTAs an SM with steps of 32 positions (84 against 76 us),
+// 16 or 32 positions at a time within a step (82, 78), copies that run ahead into the
+// next part (79: the other CTAs of the SM cover the gap already).
 //
 // Fragments.  Positions are the M of both products (S^T = K Q^T, 16 positions x
 // 8 rows; O^T = V^T P^T, 16 values x 8 rows), so eight rows waste nothing.

@@ -14,9 +14,10 @@
 // and a range of positions, widened in tiles of KT and worked on in parts of 64.
 // Sixteen warps:
 //   0..7    softmax, four warps to each 128 rows: scores out of tensor memory,
-//           weights back into it in the scores' place
-//   8..14   widen K and V codes from HBM straight into swizzled operand tiles
-//           (two stages each) and lay out the tiles' scales
+//           weights back into it in the scores' place; at the end the results
+//   8..14   (and 4..7 at D = 256, which has one row set) widen K and V codes from
+//           HBM straight into swizzled operand tiles (two stages each, loaded a
+//           tile ahead) and lay out the tiles' scales
 //   15      issues the MMAs: S = Q K^T (both operands in shared
 //           memory), O += P V (P in tensor memory, V read down its rows, which
 //           is the transposed operand that the second product needs)
@@ -31,7 +32,20 @@
 // 16x256b shape: a thread then needs a quarter of a part's scales, not all.
 // (Parts of 128 with one score buffer read less, but then every part's softmax
 // waits for the product before it and the scores after that: 6270 cycles for
-// 128 positions.)
+// 128 positions.)  At D = 256 a widened tile serves only 128 rows, and the widening
+// bounds it: 3300 cycles for 64 positions, where the products take 1300.
+//
+// Measured, graph replay: 4-bit, D = 128, a prompt of 8192 against itself with 32
+// query heads over 8: 713 us, 771 TFLOP/s, 0.47 of the measured bf16 rate; 5200 cycles
+// for 128 positions and two row sets, of which the products with their hand-overs
+// alone (nothing widened, no exponentials) take 3700; some 12 us of every CTA are its
+// start (block, barriers, queries: 5) and end (last products, results: 3) and
+// the filling of its pipeline.
+//
+// Tried and slower: 24 warps with a pair to each row quarter, half the columns each
+// (6380 cycles); weights computed against the reference of the part before while the
+// maximum is found (6654); at D = 256, parts dealt to two softmax groups in turn (as
+// fast: the softmax does not bound it).
 //
 // D order.  Widening gives codes in pairs (i, i + C/2) of C; queries are laid
 // out in the same order, and O's columns are put back when it is stored.

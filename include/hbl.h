@@ -395,8 +395,10 @@ HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_bat
  * [rows x num_heads] or NULL.  num_heads a multiple of num_kv_heads, at most
  * 65535.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
  * past it are left out and reported); max_kv: about the longest sequence (0:
- * unknown), a hint that only speed depends on.  Products are exact, sums and
- * softmax are fp32; the probabilities that weight V are rounded to fp16. */
+ * unknown), a hint that only speed depends on.  Codes and queries enter the
+ * products exactly (few rows: queries below 2^-31 of their row's largest value
+ * to within 2^-39 of it), sums and softmax are fp32; the probabilities that weight
+ * V are rounded to fp16. */
 typedef struct {
     const uint16_t* Q;
     int64_t q_row_stride, q_head_stride;
@@ -409,7 +411,7 @@ typedef struct {
 } hbl_kv_attn;
 
 /* Workspace bytes of hbl_kv_attention for these sizes (only they are read, no
- * pointer).  Calls that may run at the same time need a workspace each. */
+ * pointer); may be 0, then ws may be NULL.  Calls that may run at the same time need a workspace each. */
 HBL_API hbl_status hbl_kv_attention_workspace(const hbl_kv_cache* cache,
                                               const hbl_kv_batch* batch, const hbl_kv_attn* attn,
                                               size_t* bytes);
