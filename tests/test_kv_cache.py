@@ -361,6 +361,43 @@ def test_attention_of_many_sequences(rows, group):
 
 
 @gpu
+@pytest.mark.parametrize("D,bits", [(32, 8), (64, 4), (256, 3)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 30)])
+def test_attention_of_many_chunks(D, bits, causal, window):
+    # more chunked sequences than a warp has lanes, uneven, short and empty ones among
+    # them, so that row blocks of all of them are put in order
+    lens = [(53 * i) % 170 + 9 for i in range(70)]
+    new = [0 if i % 9 == 4 else min(n, 7 + (29 * i) % 90) for i, n in enumerate(lens)]
+    c = ref.Case(new, lens, heads=8, kv_heads=2, D=D, bits=bits, page=16, seed=D, extra_rows=1)
+    O, lse = attend(c, max_rows=max(new), causal=causal, window=window)
+    ref.check_attention(c, O, lse, causal=causal, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("group", [33, 128, 300])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_of_wide_groups(group, D):
+    # one token's query heads fill a row block, or more than one
+    c = ref.Case([1, 1, 3, 0, 2], [200, 1, 90, 5, 700], heads=group, kv_heads=1, D=D, bits=4,
+                 page=32, seed=group, extra_rows=1)
+    ref.check_attention(c, *attend(c, max_rows=3))
+    one = ref.Case([1], [1500], heads=group, kv_heads=1, D=D, bits=2, page=32, seed=group)
+    ref.check_attention(one, *attend(one))
+
+
+@gpu
+@pytest.mark.parametrize("new", [[1, 2, 1], [40, 1, 130]])
+def test_rows_before_the_first_sequence(new):
+    c = ref.Case(new, [200, 50, 131], heads=4, kv_heads=2, D=64, bits=4, seed=1, extra_rows=3)
+    want, _ = attend(c)
+    c.cu += 3
+    c.q = c.q.roll(3, 0)
+    out = torch.full_like(c.q, 7.0)
+    hbl.kv_attention(c.q, c.cache, *c.batch, out=out)
+    assert torch.equal(out[3:], want[:-3]) and bool((out[:3] == 7).all())
+
+
+@gpu
 def test_attention_under_a_wide_block_table():
     # a table with room for 2^30 positions a sequence: the plan goes by its width, the
     # work by the lengths
