@@ -802,6 +802,8 @@ static hbl_status check_kv_attn(const hbl_kv_cache* cache, const hbl_kv_batch* b
     if (a->num_heads < 1 || a->num_heads % cache->num_kv_heads != 0 || a->num_heads > 65535 ||
         a->max_rows < 0 || a->max_kv < 0)
         return HBL_ERR_SHAPE;
+    // (rows of all heads are counted in 32 bits)
+    if ((int64_t)batch->rows * a->num_heads > 0x7fffffffll - 4095) return HBL_ERR_SHAPE;
     return HBL_OK;
 }
 static KvAttn kv_attn_of(const hbl_kv_cache* c, const hbl_kv_batch* b, const hbl_kv_attn* a) {

@@ -393,7 +393,7 @@ HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_bat
  * sequence's length are never used, whatever they hold.
  * Q, O: bf16, strided as K above (O must not overlap Q); lse: fp32
  * [rows x num_heads] or NULL.  num_heads a multiple of num_kv_heads, at most
- * 65535.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
+ * 65535; rows * num_heads <= 2^31 - 4096.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
  * past it are left out and reported); max_kv: about the longest sequence (0:
  * unknown), a hint that only speed depends on.  Codes and queries enter the
  * products exactly (few rows: queries below 2^-31 of their row's largest value

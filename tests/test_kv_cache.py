@@ -80,7 +80,7 @@ def test_call_arguments_are_checked_on_the_host():
     assert _read(K=None) == 1 and _read(V=A + 8) == 3 and _read(fp32=2) == 1
     assert _attend(scale=math.nan) == 1 and _attend(window=-1) == 1 and _attend(causal=2) == 1
     assert _attend(num_heads=3) == 2 and _attend(num_heads=0) == 2 and _attend(max_rows=-1) == 2
-    assert _attend(max_kv=-1) == 2
+    assert _attend(max_kv=-1) == 2 and _attend(rows=1 << 29) == 2
     assert _attend(Q=None) == 1 and _attend(O=A + 8) == 3 and _attend(lse=A + 2) == 3
     assert _attend(q_row_stride=252) == 3 and _attend(o_head_stride=4) == 3
     lib = hbl.lib()
