@@ -624,6 +624,8 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
         o_row, o_head = _kv_rows(out, cache, "out", heads)
         if out.shape[0] != rows:
             raise ValueError("out must have Q's shape")
+        if (rows > 1 and o_row == 0) or (heads > 1 and o_head == 0):
+            raise ValueError("out must not be expanded: its rows and heads would overlap")
     lse = cache.k_scales.new_empty((rows, heads)) if want_lse else None
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
     args = _pack_attn(Q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,

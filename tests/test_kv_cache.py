@@ -626,3 +626,7 @@ def test_binding_refusals_on_the_device():
         hbl.KvCache(c.cache.k_codes, c.cache.k_scales, c.cache.v_codes, c.cache.v_scales, 100)
     with pytest.raises(hbl.HblError):
         hbl.kv_attention(torch.zeros(2, 3, 64, dtype=torch.bfloat16, device=DEV), c.cache, *c.batch)
+    one = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for out in (one.expand(2, 2, 64), one[:, :1].expand(2, 2, 64)):
+        with pytest.raises(ValueError):
+            hbl.kv_attention(c.q, c.cache, *c.batch, out=out)
