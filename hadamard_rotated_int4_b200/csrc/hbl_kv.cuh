@@ -158,21 +158,33 @@ __device__ __forceinline__ bool mbar_wait_clock(uint32_t bar, uint32_t parity,
 // ------------------------------------------------------------ the paged batch
 
 // One sequence of the batch: rows [r0, r1) of the packed new rows, `len`
-// positions in all; row t stands at position len - (r1 - r0) + (t - r0) (negative
-// for rows that the length does not reach).  Descriptors outside their bounds
-// are clamped, so nothing out of range is ever addressed, and `bad` is set.
+// positions in all; row t stands at position first + (t - r0) (negative for rows
+// that the length does not reach).  Of descriptors outside their bounds the rows
+// and positions that do not exist are cut off, so nothing out of range is ever
+// addressed, and `bad` is set; the others stay where the descriptors put them:
+// a row moved to another position would take the place of one that is cached there.
 struct KvSeq {
-    int r0, r1, len;
+    int r0, r1, first, len;
     bool bad;
 };
 __device__ __forceinline__ KvSeq kv_seq_checked(const KvBatch& kb, int page_size, int c0, int c1,
                                                 int n) {
-    KvSeq s;
+    const int cap = kb.pages_per_seq * page_size;  // (at most 2^31 - 4096)
+    KvSeq s = {c0, c1, 0, n, false};
+    s.bad = c0 < 0 || c1 < c0 || c1 > kb.rows || (unsigned)n > (unsigned)cap;
+    if (!s.bad) {
+        s.first = n - (c1 - c0);
+        return s;
+    }
     s.r0 = min(max(c0, 0), kb.rows);
     s.r1 = min(max(c1, s.r0), kb.rows);
-    const int64_t cap = (int64_t)kb.pages_per_seq * page_size;
-    s.len = (int)min((int64_t)max(n, 0), cap);
-    s.bad = s.r0 != c0 || s.r1 != c1 || s.len != n;
+    s.len = min(max(n, 0), cap);
+    const int64_t first = (int64_t)n - c1 + s.r0;  // row t at n - (c1 - t)
+    // rows past the table
+    if (first + (s.r1 - s.r0) > cap)
+        s.r1 = s.r0 + (int)max((int64_t)cap - first, (int64_t)0);
+    // (all of them before position 0: at any negative one)
+    s.first = (int)min(max(first, -(int64_t)kb.rows), (int64_t)cap);
     return s;
 }
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {

@@ -57,7 +57,7 @@ __device__ __forceinline__ Place place_of(const KvCache& c, const KvBatch& kb, i
     const KvSeq s = kv_seq_of_row(kb, c.page_size, t, &b, &bad);
     if (bad) report_status(status, HBL_ERR_INVALID_ARG);
     if (b >= kb.num_seqs) return p;  // behind the last sequence
-    const int pos = s.len - (s.r1 - s.r0) + (t - s.r0);
+    const int pos = s.first + (t - s.r0);
     p.in_seq = t >= s.r0 && t < s.r1;
     if (p.in_seq && pos >= 0) {
         const int pi = pos / c.page_size;

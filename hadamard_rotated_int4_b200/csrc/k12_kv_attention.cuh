@@ -44,7 +44,7 @@ __device__ __forceinline__ Rows rows_of(const KvBatch& kb, int page_size, const 
     Rows r;
     r.row0 = s.r0;
     r.n = min(s.r1 - s.r0, a.max_rows);
-    r.first = s.len - (s.r1 - s.r0);
+    r.first = s.first;
     r.len = s.len;
     r.bad = s.bad || r.n < s.r1 - s.r0;
     return r;

@@ -358,8 +358,9 @@ typedef struct {
  * cu_seqlens must not decrease and must stay in [0, rows]; 0 <= kv_lens[b] <=
  * pages_per_seq * page_size; the first ceil(kv_lens[b] / page_size) entries of
  * block_table[b] name pages of the cache.  Violations are memory-safe: the
- * offending rows, positions or pages are left out and dev_status (if given)
- * becomes HBL_ERR_INVALID_ARG.  Entries past a sequence's length are not used. */
+ * offending rows, positions or pages are left out (a row past the table's last
+ * position is neither written nor attended from; the others keep their places) and
+ * dev_status (if given) becomes HBL_ERR_INVALID_ARG.  Entries past a sequence's length are not used. */
 typedef struct {
     const int32_t* cu_seqlens;  /* [num_seqs + 1] */
     const int32_t* kv_lens;     /* [num_seqs] */
