@@ -415,7 +415,10 @@ def kv_quant(X, bits, eps=1e-5, out=None, status=None):
 
 # ------------------------------------------------------- paged low-bit KV cache
 # These calls run once per layer and token, so their marshalling is kept short:
-# the structs are packed bytes, and the stream is asked for by device index.
+# the structs are packed bytes, the stream is asked for by device index, and torch
+# is looked up by the first KvCache (without which there is no call), not by each call.
+
+_torch = None
 
 _pack_cache = struct.Struct("@PPPPiiiii4x").pack         # hbl_kv_cache
 _pack_batch = struct.Struct("@PPPiii4x").pack           # hbl_kv_batch
@@ -424,15 +427,31 @@ _pack_attn = struct.Struct("@PqqPqqPiiifii").pack       # hbl_kv_attn
 
 class KvCache:
     """A paged low-bit K/V cache: uint8 codes [pages, heads, page_size, D*bits/8]
-    and fp32 scales [pages, heads, page_size], for K and for V (hbl_kv_cache)."""
+    and fp32 scales [pages, heads, page_size], for K and for V (hbl_kv_cache).
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "num_pages", "num_kv_heads",
-                 "page_size", "head_dim", "bits", "device", "_index", "_args")
+    Its tensors and sizes are fixed (a larger pool is another KvCache): their addresses
+    are packed once, for all calls.  A call on a cache whose tensors' memory has been
+    resized or exchanged since is refused."""
+
+    __slots__ = ("_tensors", "_sizes", "_device", "_index", "_at", "_args")
+
+    k_codes = property(lambda self: self._tensors[0])
+    k_scales = property(lambda self: self._tensors[1])
+    v_codes = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+    num_pages = property(lambda self: self._sizes[0])
+    num_kv_heads = property(lambda self: self._sizes[1])
+    page_size = property(lambda self: self._sizes[2])
+    head_dim = property(lambda self: self._sizes[3])
+    bits = property(lambda self: self._sizes[4])
+    device = property(lambda self: self._device)
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim):
-        import torch
+        global _torch
+        if _torch is None:
+            import torch as _torch
 
-        u8, f32 = torch.uint8, torch.float32
+        u8, f32 = _torch.uint8, _torch.float32
         if not (k_codes.dtype is u8 and v_codes.dtype is u8 and k_scales.dtype is f32 and
                 v_scales.dtype is f32 and k_codes.is_cuda and k_codes.is_contiguous() and
                 v_codes.is_contiguous() and k_scales.is_contiguous() and
@@ -446,20 +465,19 @@ class KvCache:
                 v_codes.shape != code_shape or v_scales.shape != shape:
             raise ValueError("codes must be [pages, heads, page_size, D*bits/8] and scales "
                              "[pages, heads, page_size], alike for K and V")
-        self.device = device = k_codes.device
+        self._device = device = k_codes.device
         if not device == v_codes.device == k_scales.device == v_scales.device:
             raise ValueError("the cache's tensors must be on one device")
-        self.num_pages, self.num_kv_heads, self.page_size = shape
-        self.head_dim = head_dim = int(head_dim)
-        self._index = device.index
+        head_dim = int(head_dim)
         nbytes = code_shape[3]
-        self.bits = bits = nbytes * 8 // head_dim if head_dim > 0 else 0
+        bits = nbytes * 8 // head_dim if head_dim > 0 else 0
         if head_dim < 1 or kv_code_bytes(head_dim, bits) != nbytes:
             raise ValueError("the codes' last dimension must be head_dim * bits / 8 bytes")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
-                                                                   v_scales)
-        self._args = _pack_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                 v_scales.data_ptr(), shape[0], shape[2], shape[1], head_dim, bits)
+        self._index = device.index
+        self._tensors = (k_codes, k_scales, v_codes, v_scales)
+        self._sizes = (shape[0], shape[1], shape[2], head_dim, bits)
+        self._at = at = tuple([t.data_ptr() for t in self._tensors])
+        self._args = _pack_cache(*at, shape[0], shape[2], shape[1], head_dim, bits)
 
 
 def kv_cache_alloc(num_pages, page_size, num_kv_heads, head_dim, bits, device):
@@ -475,11 +493,9 @@ def kv_cache_alloc(num_pages, page_size, num_kv_heads, head_dim, bits, device):
 
 def _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows):
     """hbl_kv_batch of int32 CUDA tensors on the cache's device."""
-    import torch
-
-    i32, device = torch.int32, cache.device
+    i32, device = _torch.int32, cache._device
     for t in (cu_seqlens, kv_lens, block_table):
-        if not isinstance(t, torch.Tensor) or t.dtype is not i32 or t.device != device or \
+        if not isinstance(t, _torch.Tensor) or t.dtype is not i32 or t.device != device or \
                 not t.is_contiguous():
             _dev(t, i32, "each of cu_seqlens, kv_lens and block_table")
             raise ValueError("cu_seqlens, kv_lens and block_table must be on the cache's device")
@@ -493,17 +509,15 @@ def _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows):
 
 def _kv_rows(t, cache, name, heads=None):
     """Checks a strided bf16 [rows, heads, D] tensor; returns its strides."""
-    import torch
-
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or \
-            t.device != cache.device:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch.Tensor) or t.dtype is not _torch.bfloat16 or \
+            t.device != cache._device:
+        if not isinstance(t, _torch.Tensor) or not t.is_cuda:
             raise TypeError("%s must be a CUDA tensor" % name)
-        if t.dtype != torch.bfloat16:
-            raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+        if t.dtype != _torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (name, _torch.bfloat16, t.dtype))
         raise ValueError("%s must be on the cache's device" % name)
     shape = t.shape
-    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
+    if len(shape) != 3 or shape[2] != cache._sizes[3] or (heads is not None and shape[1] != heads):
         raise ValueError("%s must be [rows, heads, head_dim] like the cache" % name)
     sr, sh, sd = t.stride()
     if sd != 1:
@@ -514,28 +528,27 @@ def _kv_rows(t, cache, name, heads=None):
 
 def _kv_call(what, cache, *args):
     """Calls the library on the cache's device and that device's current stream."""
-    import torch
-
+    k, ks, v, vs = cache._tensors
+    if (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()) != cache._at:
+        raise ValueError("a tensor of the cache has been resized or exchanged")
     if _lib is None:
         lib()
     index = cache._index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
+    stream = _torch._C._cuda_getCurrentRawStream(index)
+    if index == _torch._C._cuda_getDevice():
         status = _kv_calls[what](*args, stream)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(index):
             status = _kv_calls[what](*args, stream)
     if status != HBL_OK:
         raise HblError(status, what)
 
 
 def _kv_status(status, cache):
-    import torch
-
     if status is None:
         return None
-    _dev(status, torch.int32, "status")
-    if status.device != cache.device:
+    _dev(status, _torch.int32, "status")
+    if status.device != cache._device:
         raise ValueError("status must be on the cache's device")
     return status.data_ptr()
 
@@ -543,8 +556,8 @@ def _kv_status(status, cache):
 def kv_cache_write(cache, K, V, cu_seqlens, kv_lens, block_table, eps=1e-5, status=None):
     """hbl_kv_cache_write: quantise the packed new rows K, V [rows, heads, D] (any
     row and head strides that are multiples of 8) into the batch's pages."""
-    ks = _kv_rows(K, cache, "K", cache.num_kv_heads)
-    vs = _kv_rows(V, cache, "V", cache.num_kv_heads)
+    ks = _kv_rows(K, cache, "K", cache._sizes[1])
+    vs = _kv_rows(V, cache, "V", cache._sizes[1])
     rows = K.shape[0]
     if V.shape[0] != rows:
         raise ValueError("K and V must have the same shape")
@@ -557,32 +570,30 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
                   status=None):
     """hbl_kv_cache_read: the last cu_seqlens[b+1] - cu_seqlens[b] positions of each
     sequence as (K, V) [rows, heads, D], bf16 (default) or torch.float32."""
-    import torch
-
     rows = int(rows)
-    shape = (rows, cache.num_kv_heads, cache.head_dim)
+    shape = (rows, cache._sizes[1], cache._sizes[3])
     if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        if dtype not in (torch.bfloat16, torch.float32):
+        dtype = _torch.bfloat16 if dtype is None else dtype
+        if dtype not in (_torch.bfloat16, _torch.float32):
             raise TypeError("dtype must be torch.bfloat16 or torch.float32, got %s" % dtype)
         if rows < 0:
             raise ValueError("rows must not be negative")
-        like = cache.k_scales if dtype is torch.float32 else None
+        like = cache._tensors[1] if dtype is _torch.float32 else None
         K = like.new_empty(shape) if like is not None else \
-            torch.empty(shape, dtype=dtype, device=cache.device)
-        V = torch.empty_like(K)
+            _torch.empty(shape, dtype=dtype, device=cache._device)
+        V = _torch.empty_like(K)
     else:
         K, V = out
         dtype = K.dtype if dtype is None else dtype
-        if dtype not in (torch.bfloat16, torch.float32):
+        if dtype not in (_torch.bfloat16, _torch.float32):
             raise TypeError("out must be torch.bfloat16 or torch.float32, got %s" % dtype)
         for t in (K, V):
             _dev(t, dtype, "out")
-            if tuple(t.shape) != shape or t.device != cache.device:
+            if tuple(t.shape) != shape or t.device != cache._device:
                 raise ValueError("out must be two [rows, heads, D] tensors on the cache's device")
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
     _kv_call("hbl_kv_cache_read", cache, cache._args, batch, K.data_ptr(), V.data_ptr(),
-             1 if dtype == torch.float32 else 0, _kv_status(status, cache))
+             1 if dtype == _torch.float32 else 0, _kv_status(status, cache))
     return K, V
 
 
@@ -613,12 +624,10 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     (about the longest sequence) are host-side sizes that the launch is planned
     with; without them the row count and the block table's width are taken.
     Returns O (out if given), with want_lse also lse fp32 [rows, q heads]."""
-    import torch
-
     q_row, q_head = _kv_rows(Q, cache, "Q")
     rows, heads, D = Q.shape
     if out is None:
-        out = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty((rows, heads, D))
+        out = _torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty((rows, heads, D))
         o_row, o_head = heads * D, D
     else:
         o_row, o_head = _kv_rows(out, cache, "out", heads)
@@ -626,7 +635,7 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
             raise ValueError("out must have Q's shape")
         if (rows > 1 and o_row == 0) or (heads > 1 and o_head == 0):
             raise ValueError("out must not be expanded: its rows and heads would overlap")
-    lse = cache.k_scales.new_empty((rows, heads)) if want_lse else None
+    lse = cache._tensors[1].new_empty((rows, heads)) if want_lse else None
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
     args = _pack_attn(Q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,
                       lse.data_ptr() if want_lse else 0, heads, max_rows or 0, max_kv or 0,
@@ -634,9 +643,9 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     if ws is None:
         nbytes = _kv_attention_bytes(cache._args, batch, args)
         if nbytes:
-            ws = cache.k_codes.new_empty(nbytes)
+            ws = cache._tensors[0].new_empty(nbytes)
     else:
-        if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != cache.device or \
+        if not isinstance(ws, _torch.Tensor) or not ws.is_cuda or ws.device != cache._device or \
                 not ws.is_contiguous():
             raise ValueError("ws must be a contiguous tensor on the cache's device")
         nbytes = ws.numel() * ws.element_size()

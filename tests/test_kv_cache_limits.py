@@ -84,3 +84,21 @@ def test_rows_outside_the_bounds_are_left_out_where_they_stand(cu, lens, rows):
         alone = hbl.kv_attention(c.q[t:t + 1].contiguous(), c.cache, *one)
         # (both within the attention's tolerance, mostly the output's half step of 2^-8)
         assert torch.allclose(O[t].float(), alone[0].float(), rtol=2.0 ** -6, atol=1e-3)
+
+# ------------------------------------------------------------- a cache's tensors
+
+@gpu
+def test_a_cache_keeps_the_tensors_it_was_made_of():
+    c = ref.Case([2], [20], heads=2, kv_heads=2, D=64, bits=4)
+    cache = c.cache
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales", "num_pages", "num_kv_heads",
+                 "page_size", "head_dim", "bits", "device"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
+    # a tensor whose memory has moved is refused, by each call
+    cache.v_codes.resize_(64, *cache.v_codes.shape[1:])
+    for call in (lambda: hbl.kv_cache_write(cache, c.k, c.v, *c.batch),
+                 lambda: hbl.kv_cache_read(cache, *c.batch, c.rows),
+                 lambda: hbl.kv_attention(c.q, cache, *c.batch)):
+        with pytest.raises(ValueError):
+            call()
