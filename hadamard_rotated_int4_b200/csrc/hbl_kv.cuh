@@ -158,50 +158,50 @@ __device__ __forceinline__ bool mbar_wait_clock(uint32_t bar, uint32_t parity,
 // ------------------------------------------------------------ the paged batch
 
 // One sequence of the batch: rows [r0, r1) of the packed new rows, `len`
-// positions in all; row t stands at position first + (t - r0) (negative for rows
-// that the length does not reach).  Of descriptors outside their bounds the rows
-// and positions that do not exist are cut off, so nothing out of range is ever
-// addressed, and `bad` is set; the others stay where the descriptors put them:
-// a row moved to another position would take the place of one that is cached there.
+// positions in all; row t stands at position len - (c1 - t) = first + (t - r0), c1 the
+// end that the descriptors give (negative for rows that the length does not reach).
+// Of descriptors outside their bounds the rows and positions that do not exist are cut
+// off, so nothing out of range is ever addressed, and `bad` is set; the others stay
+// where the descriptors put them: a row moved to another position would take the place
+// of one that is cached there.
 struct KvSeq {
     int r0, r1, first, len;
     bool bad;
 };
-__device__ __forceinline__ KvSeq kv_seq_checked(const KvBatch& kb, int page_size, int c0, int c1,
-                                                int n) {
-    const int cap = kb.pages_per_seq * page_size;  // (at most 2^31 - 4096)
-    KvSeq s = {c0, c1, 0, n, false};
-    s.bad = c0 < 0 || c1 < c0 || c1 > kb.rows || (unsigned)n > (unsigned)cap;
-    if (!s.bad) {
-        s.first = n - (c1 - c0);
-        return s;
-    }
+__device__ __forceinline__ bool kv_bad(const KvBatch& kb, int cap, int c0, int c1, int n) {
+    return c0 < 0 || c1 < c0 || c1 > kb.rows || (unsigned)n > (unsigned)cap;
+}
+__device__ __forceinline__ int kv_capacity(const KvBatch& kb, int page_size) {
+    return kb.pages_per_seq * page_size;  // (at most 2^31 - 4096)
+}
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {
+    const int c0 = __ldg(kb.cu + b), c1 = __ldg(kb.cu + b + 1), n = __ldg(kb.lens + b);
+    const int cap = kv_capacity(kb, page_size);
+    KvSeq s;
     s.r0 = min(max(c0, 0), kb.rows);
     s.r1 = min(max(c1, s.r0), kb.rows);
     s.len = min(max(n, 0), cap);
-    const int64_t first = (int64_t)n - c1 + s.r0;  // row t at n - (c1 - t)
-    // rows past the table
-    if (first + (s.r1 - s.r0) > cap)
-        s.r1 = s.r0 + (int)max((int64_t)cap - first, (int64_t)0);
-    // (all of them before position 0: at any negative one)
-    s.first = (int)min(max(first, -(int64_t)kb.rows), (int64_t)cap);
+    // (where there are rows, r0 < c1: no overflow; where n < 0, all have no place)
+    s.first = (int)((unsigned)max(n, 0) - (unsigned)c1 + (unsigned)s.r0);
+    if (n > cap) s.r1 = max(s.r0, min(s.r1, c1 - (n - cap)));  // rows past the table
+    s.bad = kv_bad(kb, cap, c0, c1, n);
     return s;
 }
-__device__ __forceinline__ KvSeq kv_seq(const KvBatch& kb, int page_size, int b) {
-    return kv_seq_checked(kb, page_size, __ldg(kb.cu + b), __ldg(kb.cu + b + 1),
-                          __ldg(kb.lens + b));
-}
 
-// The sequence of packed row t, found by the whole warp (every lane calls it
-// with the same t): that whose rows end first behind t.  One round of loads for 32
-// sequences: their ends and lengths come together, and the found one's are handed
-// round.  b = kb.num_seqs for a row behind the last sequence; bad is set on lanes
-// that met a descriptor outside its bounds on the way.
-__device__ __forceinline__ KvSeq kv_seq_of_row(const KvBatch& kb, int page_size, int t, int* b,
-                                               bool* bad) {
-    const int lane = threadIdx.x & 31;
-    KvSeq s = {};
-    *b = kb.num_seqs;
+// The sequence and position of packed row t, found by the whole warp (every lane calls
+// it with the same t): the sequence is that whose rows end first behind t.  One round
+// of loads for 32 sequences: their ends and lengths come together, and the found one's
+// are handed round.  in_seq is false for a row before the first sequence, behind the
+// last one or past the table; pos is below the sequence's clamped length, and negative
+// for a row without a place.  bad is set on lanes that met a descriptor outside its
+// bounds on the way.
+struct KvRow {
+    int b, pos;
+    bool in_seq;
+};
+__device__ __forceinline__ KvRow kv_row(const KvBatch& kb, int page_size, int t, bool* bad) {
+    const int lane = threadIdx.x & 31, cap = kv_capacity(kb, page_size);
+    KvRow r = {kb.num_seqs, 0, false};
     int before = __ldg(kb.cu);  // where the sequences looked at begin
     for (int i = 0; i < kb.num_seqs; i += 32) {
         const bool in = i + lane < kb.num_seqs;
@@ -212,18 +212,19 @@ __device__ __forceinline__ KvSeq kv_seq_of_row(const KvBatch& kb, int page_size,
         // past the table), whether row t is theirs or not
         int start = __shfl_up_sync(0xffffffffu, end, 1);
         if (lane == 0) start = before;
-        if (in && kv_seq_checked(kb, page_size, start, end, n).bad) *bad = true;
+        if (in && kv_bad(kb, cap, start, end, n)) *bad = true;
         if (after != 0) {
             const int k = __ffs(after) - 1;
             const int c1 = __shfl_sync(0xffffffffu, end, k), len = __shfl_sync(0xffffffffu, n, k);
-            const int c0 = k > 0 ? __shfl_sync(0xffffffffu, end, k - 1) : before;
-            *b = i + k;
-            s = kv_seq_checked(kb, page_size, c0, c1, len);
+            const int c0 = __shfl_sync(0xffffffffu, start, k);
+            r.b = i + k;
+            r.pos = max(len, 0) - (c1 - t);
+            r.in_seq = t >= c0 && r.pos < cap;
             break;
         }
         before = __shfl_sync(0xffffffffu, end, 31);
     }
-    return s;
+    return r;
 }
 
 // The page that holds position pos of sequence b, or -1 if the block table names

@@ -52,18 +52,15 @@ __device__ __forceinline__ Place place_of(const KvCache& c, const KvBatch& kb, i
     Place p;
     p.base = 0;
     p.in_seq = p.ok = false;
-    int b;
     bool bad = false;
-    const KvSeq s = kv_seq_of_row(kb, c.page_size, t, &b, &bad);
+    const KvRow r = kv_row(kb, c.page_size, t, &bad);
     if (bad) report_status(status, HBL_ERR_INVALID_ARG);
-    if (b >= kb.num_seqs) return p;  // behind the last sequence
-    const int pos = s.first + (t - s.r0);
-    p.in_seq = t >= s.r0 && t < s.r1;
-    if (p.in_seq && pos >= 0) {
-        const int pi = pos / c.page_size;
-        const int page = kv_page(kb, c.num_pages, b, pi);
+    p.in_seq = r.in_seq;
+    if (r.in_seq && r.pos >= 0) {
+        const int pi = r.pos / c.page_size;
+        const int page = kv_page(kb, c.num_pages, r.b, pi);
         if (page >= 0) {
-            p.base = (int64_t)page * c.heads * c.page_size + (pos - pi * c.page_size);
+            p.base = (int64_t)page * c.heads * c.page_size + (r.pos - pi * c.page_size);
             p.ok = true;
         } else if ((threadIdx.x & 31) == 0) {
             report_status(status, HBL_ERR_INVALID_ARG);

@@ -93,12 +93,12 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) join_ranges_kernel(KvCache c, KvBatch kb, KvAttn a,
                                                                Plan pl, const float* part) {
     const int t = (int)blockIdx.x, head = (int)blockIdx.y, h = head / a.group;
-    int b, count = 0, row = 0;
+    int count = 0, row = 0;
     bool bad = false;
-    const KvSeq q = kv_seq_of_row(kb, c.page_size, t, &b, &bad);
+    const KvRow q = kv_row(kb, c.page_size, t, &bad);
     Rows s = {};
-    if (b < kb.num_seqs && t >= q.r0) {
-        s = rows_of(kb, c.page_size, a, b);
+    if (q.in_seq) {
+        s = rows_of(kb, c.page_size, a, q.b);
         const int nr = s.n * a.group;
         row = (t - s.row0) * a.group + head - h * a.group;
         const int r0 = row / pl.block_rows * pl.block_rows;
