@@ -22,12 +22,16 @@ using KvHalf = typename std::conditional<(8 * B <= 32), uint32_t, uint64_t>::typ
 
 // Quantises a row spread over D/16 neighbouring lanes (bf16 bits in raw):
 // gamma = max|x| over those lanes, inv = Qp / (gamma + eps) (one division),
-// u = rhe(x * inv) + 2^(B-1), each product rounded once by an fma with
-// 1.5 * 2^23.  No clamp is needed: |x| <= gamma, so |x * inv| <= Qp up to the
-// rounding of inv (well under half a unit).  Returns gamma / Qp.
+// u = clip(rhe(x * inv), -Qp - 1, Qp) + 2^(B-1), each product rounded once by an
+// fma with 1.5 * 2^23.  Where inv is finite, no product needs the clip: |x| <= gamma,
+// so |x * inv| <= Qp up to the rounding of inv (well under half a unit).  It is infinite
+// exactly where gamma + eps <= Qp * 2^-128, with eps = 0 or nearly: then *over is set,
+// and the codes are kv_ends16's, from the row loaded once more (kept in registers for
+// that rare case, it costs K11 spills).  Returns gamma / Qp.
 // Every lane of the warp calls it (the max goes through shuffles).
 template <int D, int B>
-__device__ __forceinline__ float kv_quant16(const uint4 (&raw)[2], float eps, KvHalf<B> (&h)[2]) {
+__device__ __forceinline__ float kv_quant16(const uint4 (&raw)[2], float eps, KvHalf<B> (&h)[2],
+                                            bool* over) {
     constexpr int QP = (1 << (B - 1)) - 1;
     constexpr int32_t kMagicBits = 0x4B400000;  // 1.5 * 2^23
     const float qp = (float)QP;
@@ -46,7 +50,8 @@ __device__ __forceinline__ float kv_quant16(const uint4 (&raw)[2], float eps, Kv
 #pragma unroll
     for (int o = 1; o < D / kKvVpl; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
     const float den = __fadd_rn(g, eps);
-    const float inv = den > 0.f ? __fdiv_rn(qp, den) : 0.f;
+    *over = den <= qp * 0x1p-128f;
+    const float inv = __fdiv_rn(qp, den);
     h[0] = 0;
     h[1] = 0;
 #pragma unroll
@@ -56,6 +61,24 @@ __device__ __forceinline__ float kv_quant16(const uint4 (&raw)[2], float eps, Kv
         h[i / 8] |= (KvHalf<B>)code << (B * (i % 8));
     }
     return __fdiv_rn(g, qp);
+}
+
+// Codes of 16 values for an infinite inv: the clip's ends by their signs, zero for zeros
+// (gamma + eps = 0 among them).
+template <int B>
+__device__ __forceinline__ void kv_ends16(const uint4 (&raw)[2], KvHalf<B> (&h)[2]) {
+    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                           raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    h[0] = 0;
+    h[1] = 0;
+#pragma unroll
+    for (int i = 0; i < kKvVpl; ++i) {
+        const uint32_t x = w[i / 2] >> (16 * (i % 2));
+        const uint32_t code = (x & 0x7fffu) == 0    ? 1u << (B - 1)
+                              : (x & 0x8000u) != 0 ? 0u
+                                                   : (1u << B) - 1u;
+        h[i / 8] |= (KvHalf<B>)code << (B * (i % 8));
+    }
 }
 
 // Stores lane li's 16 codes of the row at dst (D*B/8 bytes).  Every lane of the

@@ -94,22 +94,29 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas) write_kernel(KvCache c, 
         const uint16_t* const k0 = x.k + (int64_t)t * x.k_row + li * kKvVpl;
         const uint16_t* const v0 =
             x.v + (int64_t)t * x.v_row - (int64_t)c.heads * x.v_head + li * kKvVpl;
-#pragma unroll
-        for (int step = 0; step < kSteps; ++step) {  // the rows load while their place is found
+        auto load = [&](int step, uint4 (&to)[2]) {
             const int r = first + step * RPW + sub;  // K heads, then V heads
             const bool isv = r >= c.heads;
             const uint4* s = reinterpret_cast<const uint4*>((isv ? v0 : k0) +
                                                             r * (isv ? x.v_head : x.k_head));
-            raw[step][0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
-            raw[step][1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
-        }
+            to[0] = r < last ? s[0] : make_uint4(0, 0, 0, 0);
+            to[1] = r < last ? s[1] : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) load(step, raw[step]);  // while their place is found
         const Place p = place_of(c, kb, t, status);
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
             if (first + step * RPW >= last) break;
             const int r = first + step * RPW + sub;
             KvHalf<B> h[2];
-            const float scale = kv_quant16<D, B>(raw[step], eps, h);
+            bool over;
+            const float scale = kv_quant16<D, B>(raw[step], eps, h, &over);
+            if (over) {
+                uint4 again[2];
+                load(step, again);
+                kv_ends16<B>(again, h);
+            }
             const bool ok = p.ok && r < last, isv = r >= c.heads;
             const int64_t row = p.base + (int64_t)(isv ? r - c.heads : r) * c.page_size;
             kv_store16<B>((isv ? c.vc : c.kc) + row * ROW_BYTES, li, h, ok);

@@ -47,18 +47,25 @@ __global__ void __launch_bounds__(kThreads) kv_quant_kernel(const uint16_t* __re
 
     for (int64_t base = warp0 * (RPW * U); base < rows; base += nwarps * (RPW * U)) {
         uint4 raw[U][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+        auto load = [&](int u, uint4 (&to)[2]) {
             const int64_t row = base + u * RPW + sub;
             const uint4* src = reinterpret_cast<const uint4*>(X + row * D + li * VPL);
-            raw[u][0] = row < rows ? src[0] : make_uint4(0, 0, 0, 0);
-            raw[u][1] = row < rows ? src[1] : make_uint4(0, 0, 0, 0);
-        }
+            to[0] = row < rows ? src[0] : make_uint4(0, 0, 0, 0);
+            to[1] = row < rows ? src[1] : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(u, raw[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = base + u * RPW + sub;
             KvHalf<B> h[2];
-            const float scale = kv_quant16<D, B>(raw[u], eps, h);
+            bool over;
+            const float scale = kv_quant16<D, B>(raw[u], eps, h, &over);
+            if (over) {
+                uint4 again[2];
+                load(u, again);
+                kv_ends16<B>(again, h);
+            }
             const bool ok = row < rows;
             kv_store16<B>(codes + row * ROW_BYTES, li, h, ok);
             if (ok && li == 0) scales[row] = scale;

@@ -319,7 +319,9 @@ HBL_API hbl_status hbl_rotate_weights(const float* W, const float* signs, int N,
  *   Qp = 2^(bits-1) - 1;  gamma = max|x|;  inv = Qp / (gamma + eps)  (one division)
  *   q = clip(rhe(x * inv), -Qp-1, Qp);  u = q + 2^(bits-1);  scales[row] = gamma / Qp
  * (the INT8 activation quantiser taken to `bits` bits and offset into the
- * unsigned range; dequantise as (u - 2^(bits-1)) * scale).
+ * unsigned range; dequantise as (u - 2^(bits-1)) * scale).  Where inv passes fp32 (a
+ * row maximum of at most Qp * 2^-128 with eps = 0 or nearly), it is infinite: values
+ * of either sign take the clip's ends, zeros q = 0.
  * X: bf16 [rows x D] (e.g. [tokens x heads x D]); bits in {2, 3, 4, 8};
  * D in {32, 64, 128, 256}; eps >= 0 finite.
  * codes: [rows x D*bits/8] bytes out: each group of 32 consecutive codes of a

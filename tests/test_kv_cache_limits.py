@@ -102,3 +102,36 @@ def test_a_cache_keeps_the_tensors_it_was_made_of():
                  lambda: hbl.kv_attention(c.q, cache, *c.batch)):
         with pytest.raises(ValueError):
             call()
+
+# ------------------------------------------------------------ rows of tiny values
+
+def tiny_rows(D):
+    """bf16 bits [8, D]: the quotient Qp / max|x| passes fp32 in some, in others just not."""
+    g = np.random.default_rng(D)
+    x = np.zeros((8, D), dtype=np.uint16)
+    x[0] = g.integers(0, 4, D)                      # the smallest subnormal numbers
+    x[1] = g.integers(0, 4, D) | 0x8000
+    x[2] = g.integers(0, 0x80, D) | (g.integers(0, 2, D) << 15)  # subnormal ones of either sign
+    x[3, 5] = 1                                     # one value, the rest zero
+    x[4] = g.integers(0, 0x0100, D) | (g.integers(0, 2, D) << 15)
+    x[5] = g.integers(0, 0x0800, D) | (g.integers(0, 2, D) << 15)
+    x[6] = g.integers(0, 0x7f00, D)                 # all sizes
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-38, 1e-5])
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_tiny_rows_quantise_as_defined(D, bits, eps):
+    x = tiny_rows(D)
+    codes, scales = oracle.kv_quant(x, bits, eps=eps)
+    dev = torch.from_numpy(x.view(np.int16).copy()).view(torch.bfloat16).to(DEV)
+    got = hbl.kv_quant(dev, bits, eps=eps)
+    assert np.array_equal(got[0].cpu().numpy(), codes)
+    assert np.array_equal(got[1].cpu().numpy().view(np.uint32), scales.view(np.uint32))
+    c = ref.Case([8], [8], heads=1, kv_heads=1, D=D, bits=bits, page=16)
+    hbl.kv_cache_write(c.cache, dev.view(8, 1, D), dev.flip(0).view(8, 1, D), *c.batch, eps=eps)
+    page = int(c.table[0, 0])
+    for pool, want in zip(pools(c.cache), (codes, scales, codes[::-1], scales[::-1])):
+        assert same_bytes(pool[page, 0, :8], torch.from_numpy(want.copy()))
