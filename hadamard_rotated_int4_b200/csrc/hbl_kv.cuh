@@ -157,6 +157,10 @@ hbl_status kv_dispatch(int D, int bits, F&& f) {
     }
 }
 
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 // ------------------------------------------------------------ waits of a pipeline
 
 // Waits for an mbarrier phase, for at most about two seconds (in SM clocks), and

@@ -83,6 +83,32 @@ __device__ __forceinline__ Split split_of(const Plan& pl, const Range& rg, int s
     return s;
 }
 
+// ---- V's scales and the reference points of a row
+// O's sum and its normaliser, with scores s and V's scales sv, both in log2:
+//   O = sum_i 2^(s_i + sv_i - M) v_i / sum_i 2^(s_i - R) * 2^(M - R).
+// M follows the largest s + sv.  Where all of V's scales lie in 2^-kFold .. 2^kFold, R is
+// M, and the second sum is that of w_i / sv_i of the weights w_i that the product needs
+// anyway; a zero scale counts as 2^kZeroFold (its codes are zeros, and only its score
+// matters; weights of 2^-126 are 2^-32 of the largest score's at most).  Past
+// that the weights of small scales, or 1 / sv, leave fp32's range.  A kernel
+// that meets such a scale takes its positions once more and sums 2^(s_i - R) apart, R the
+// largest s: an exponential a score more, and no scale is too large or too small.  What
+// it hands on is O's sum and the normaliser against one point, half way between M
+// and R (at most 150 apart): both stay in range.
+constexpr float kFold = 40.f, kZeroFold = -60.f;
+constexpr float kNoScale = -150.f;  // log2 of a zero scale apart: below every other
+__device__ __forceinline__ bool folds(float sv) {  // zero, or of 2^-kFold .. 2^kFold
+    constexpr uint32_t kLow = (uint32_t)(127 - (int)kFold) << 23;
+    constexpr uint32_t kSpan = (uint32_t)(2 * (int)kFold) << 23;
+    const uint32_t bits = __float_as_uint(sv);
+    return bits == 0 || bits - kLow <= kSpan;
+}
+__device__ __forceinline__ float lg2_any(float x) {  // subnormal x too
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Partial results of chunks: [split][packed row][query head] x (D values, m, sum, 2 unused).
 __device__ __forceinline__ int64_t part_index(const KvBatch& kb, const KvAttn& a, int split,
                                               int64_t t, int head) {

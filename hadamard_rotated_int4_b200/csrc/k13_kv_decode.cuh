@@ -8,7 +8,9 @@
 // in one pass with the running m: taking V's scale into the exponent leaves the
 // integer codes as the second product's operand, and the weights 2^(x_i - m)
 // in (0, 2^8], so that fp16 holds them (times 2^6; what is below 2^-31 of
-// the reference is lost, a term's rounding is 2^-12 of itself).
+// the reference is lost, a term's rounding is 2^-12 of itself).  Where 1 / sv or a weight
+// leaves fp32's range, which takes V scales outside 2^-40 .. 2^40, a part is worked on
+// once more with its normaliser summed apart (k12_kv_attention.cuh).
 //
 // What bounds it: the codes and scales of every visible position are read once
 // per cached head, 2*D*b/8 + 8 bytes a position (HBM), and close behind it the
@@ -144,6 +146,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
     const uint32_t ring = smem_addr(smem) + warp * St::kCount * St::kBytes;
     const uint32_t bars = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + warp * 32;
     if (lane < St::kCount) mbar_init_count(bars + 8 * lane, 1);
+    // a flag behind the first warp's barriers (at most three): V's scales need a second pass
+    const uint32_t odd_s = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + 24;
+    if (threadIdx.x == 0) sts32(odd_s, 0);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
     int done = 0;  // stages of this warp's ring that have been used
@@ -231,9 +236,13 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                     : "memory");
             }
         };
+        int next_page;
+        auto start = [&] {
 #pragma unroll
-        for (int it = 0; it < St::kCount; ++it) issue(it, page_of(it));
-        int next_page = page_of(St::kCount);
+            for (int it = 0; it < St::kCount; ++it) issue(it, page_of(it));
+            next_page = page_of(St::kCount);
+        };
+        start();
 
         // ---- Q's fragments: pair p of lane t is codes (C w + i, C w + i + C/2), C = 2H
         uint32_t q[NT][kPairs];
@@ -285,177 +294,278 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
 
         float O[NV / 2][NT][4];
         float m[NT][2], base[NT][2], l[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int k = 0; k < NV / 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) O[k][n][e] = 0.f;
-            m[n][0] = m[n][1] = -CUDART_INF_F;
-            l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
-        }
+        float ref[NT][2];  // what l counts against
         const int kslot = (g >> 1) + 4 * (g & 1);  // this lane's K rows: kslot, kslot + 8
-
-        int it = 0;
-        for (; it < steps; ++it) {
-            const int use = done + it, ring_slot = use % St::kCount;
-            const uint32_t st = ring + ring_slot * St::kBytes;
-            if (!__all_sync(0xffffffffu, mbar_wait_clock(bars + 8 * ring_slot,
-                                                         (use / St::kCount) & 1, nullptr))) {
-                if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
-                break;
+        // One pass over the part's positions; whether a wait gave up.  APART: the normaliser
+        // is summed apart; otherwise `odd` says whether it has to be.
+        bool odd = false;
+        auto pass = [&](auto apart) {
+            constexpr bool APART = decltype(apart)::value;
+            constexpr int NBP = APART ? 1 : NB;  // blocks of a step at once (few: less code)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int k = 0; k < NV / 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[k][n][e] = 0.f;
+                m[n][0] = m[n][1] = -CUDART_INF_F;
+                l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
+                ref[n][0] = ref[n][1] = -CUDART_INF_F;
             }
-            const int key0 = first + it * step;
-            const uint32_t flags = lds32(st + 2 * St::kCodes + 2 * St::kScales);
-            const bool plain = flags == (1u << (KW >> seg_shift)) - 1u && key0 >= all_lo &&
-                               key0 + KW <= min(all_hi, end);
 
-            float S[NB][NT][4];
-#pragma unroll
-            for (int blk = 0; blk < NB; ++blk) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[blk][n][e] = 0.f;
-                const uint32_t r0 = st + (16 * blk + kslot) * St::kRow;
-                uint32_t w0[kKvWords<B, NK>], w1[kKvWords<B, NK>];
-                kv_lds_codes<B, NK>(r0, t, w0);
-                kv_lds_codes<B, NK>(r0 + 8 * St::kRow, t, w1);
-                if constexpr (NK < 2 * H) {  // 8 codes of 2 bits: one half word, split in two of 4
-                    w0[0] = (w0[0] & 0xffu) | ((w0[0] & 0xff00u) << 8);
-                    w1[0] = (w1[0] & 0xffu) | ((w1[0] & 0xff00u) << 8);
+            int it = 0;
+            for (; it < steps; ++it) {
+                const int use = done + it, ring_slot = use % St::kCount;
+                const uint32_t st = ring + ring_slot * St::kBytes;
+                if (!__all_sync(0xffffffffu, mbar_wait_clock(bars + 8 * ring_slot,
+                                                             (use / St::kCount) & 1, nullptr))) {
+                    if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
+                    break;
                 }
-                constexpr int P = NK < 2 * H ? NK / 2 : H;  // pairs of a word
-                static_for<0, kKvWords<B, NK>>([&](auto ww) {
-                    constexpr int w = decltype(ww)::value;
-                    uint32_t a0[P], a1[P];
-                    kv_widen_f16<B, P>(w0[w], a0);
-                    kv_widen_f16<B, P>(w1[w], a1);
+                const int key0 = first + it * step;
+                const uint32_t flags = lds32(st + 2 * St::kCodes + 2 * St::kScales);
+                const bool plain = flags == (1u << (KW >> seg_shift)) - 1u && key0 >= all_lo &&
+                                   key0 + KW <= min(all_hi, end);
+
+#pragma unroll 1
+                for (int b0 = 0; b0 < NB; b0 += NBP) {
+                    float S[NBP][NT][4];
 #pragma unroll
-                    for (int p = 0; p < P; p += 2)
+                    for (int blk = 0; blk < NBP; ++blk) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma_f16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1], q[n][P * w + p],
-                                    q[n][P * w + p + 1]);
-                });
-            }
-            // ---- exponents
-            float mx[NT][2], rsv[NB][2];  // rsv: 1 / sv of positions kslot, kslot + 8
 #pragma unroll
-            for (int blk = 0; blk < NB; ++blk)
+                            for (int e = 0; e < 4; ++e) S[blk][n][e] = 0.f;
+                        const uint32_t r0 = st + (16 * (b0 + blk) + kslot) * St::kRow;
+                        uint32_t w0[kKvWords<B, NK>], w1[kKvWords<B, NK>];
+                        kv_lds_codes<B, NK>(r0, t, w0);
+                        kv_lds_codes<B, NK>(r0 + 8 * St::kRow, t, w1);
+                        if constexpr (NK < 2 * H) {  // 8 codes of 2 bits: a half word, in two of 4
+                            w0[0] = (w0[0] & 0xffu) | ((w0[0] & 0xff00u) << 8);
+                            w1[0] = (w1[0] & 0xffu) | ((w1[0] & 0xff00u) << 8);
+                        }
+                        constexpr int P = NK < 2 * H ? NK / 2 : H;  // pairs of a word
+                        static_for<0, kKvWords<B, NK>>([&](auto ww) {
+                            constexpr int w = decltype(ww)::value;
+                            uint32_t a0[P], a1[P];
+                            kv_widen_f16<B, P>(w0[w], a0);
+                            kv_widen_f16<B, P>(w1[w], a1);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t sc = st + 2 * St::kCodes + 4 * (16 * blk + kslot + 8 * u);
-                    const float sk = __uint_as_float(lds32(sc));
-                    // a zero scale (an all-zero row: its codes are zero too) as 2^-100
-                    const float lv = fmaxf(lg2(__uint_as_float(lds32(sc + St::kScales))), -100.f);
-                    rsv[blk][u] = ex2(-lv);
+                            for (int p = 0; p < P; p += 2)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16(S[blk][n], a0[p], a1[p], a0[p + 1], a1[p + 1],
+                                            q[n][P * w + p], q[n][P * w + p + 1]);
+                        });
+                    }
+                    // ---- exponents
+                    float mx[NT][2], rsv[NBP][2];  // rsv: 1 / sv of positions kslot, kslot + 8
+                    float step_far = 0.f;  // of this lane's positions, the largest |log2(sv)|
+#pragma unroll
+                    for (int blk = 0; blk < NBP; ++blk) {
+                        float lvs[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t sc =
+                                st + 2 * St::kCodes + 4 * (16 * (b0 + blk) + kslot + 8 * u);
+                            const float sk = __uint_as_float(lds32(sc));
+                            const float any =
+                                APART ? 0.f : lg2(__uint_as_float(lds32(sc + St::kScales)));
+                            lvs[u] = fabsf(any);
+                            const float lv = APART ? 0.f : fmaxf(any, k12::kZeroFold);
+                            rsv[blk][u] = ex2(-lv);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    S[blk][n][2 * u + e] = __fmaf_rn(
+                                        S[blk][n][2 * u + e], __fmul_rn(sk, xs[n][e]), lv);
+                        }
+                        step_far = max3(step_far, lvs[0], lvs[1]);
+                    }
+                    if (!plain) {  // what is not visible becomes -inf, whatever is stored there
+                        step_far = 0.f;
+#pragma unroll
+                        for (int blk = 0; blk < NBP; ++blk)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int slot = 16 * (b0 + blk) + kslot + 8 * u, key = key0 + slot;
+                                const bool there =
+                                    ((flags >> (slot >> seg_shift)) & 1u) != 0 && key < end;
+                                if (!there)
+                                    rsv[blk][u] = 0.f;
+                                else if (!(rsv[blk][u] >= 0x1p-40f && rsv[blk][u] <= 0x1p40f))
+                                    step_far = CUDART_INF_F;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (!(there && key >= lo[n][e] && key < hi[n][e]))
+                                            S[blk][n][2 * u + e] = -CUDART_INF_F;
+                            }
+                    }
+                    odd |= step_far > k12::kFold;
+                    auto largest = [&] {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mx[n][e] = fmaxf(S[0][n][e], S[0][n][2 + e]);
+#pragma unroll
+                                for (int blk = 1; blk < NBP; ++blk)
+                                    mx[n][e] = max3(mx[n][e], S[blk][n][e], S[blk][n][2 + e]);
+                            }
+                    };
+                    largest();
+                    if constexpr (APART) {  // the scores' own largest and sum; then V's scales
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    mx[n][e] =
+                                        fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
+                                const float to = fmaxf(ref[n][e], mx[n][e]);
+                                const float rb = to == -CUDART_INF_F ? 0.f : kShift - to;
+                                if (to != ref[n][e]) l[n][e] *= ex2(ref[n][e] - to);
+                                ref[n][e] = to;
+#pragma unroll
+                                for (int blk = 0; blk < NBP; ++blk)
+                                    l[n][e] += ex2(S[blk][n][e] + rb) + ex2(S[blk][n][2 + e] + rb);
+                            }
+#pragma unroll
+                        for (int blk = 0; blk < NBP; ++blk)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                // (stored where nothing is, it may be anything: -inf stays -inf)
+                                const uint32_t sc = st + 2 * St::kCodes + St::kScales +
+                                                    4 * (16 * (b0 + blk) + kslot + 8 * u);
+                                const float any = k12::lg2_any(__uint_as_float(lds32(sc)));
+                                const float lv = fminf(fmaxf(any, k12::kNoScale), 128.f);
+                                rsv[blk][u] = 0.f;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) S[blk][n][2 * u + e] += lv;
+                            }
+                        largest();
+                    }
+                    // each lane looks at its own positions' largest; only when one is too far
+                    // above the reference do the lanes of a row find their common one
+                    bool far = false;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            S[blk][n][2 * u + e] =
-                                __fmaf_rn(S[blk][n][2 * u + e], __fmul_rn(sk, xs[n][e]), lv);
-                }
-            if (!plain) {  // what is not visible becomes -inf, whatever is stored there
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int slot = 16 * blk + kslot + 8 * u, key = key0 + slot;
-                        const bool there =
-                            ((flags >> (slot >> seg_shift)) & 1u) != 0 && key < end;
-                        if (!there) rsv[blk][u] = 0.f;
+                        far |= mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
+                    if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (!(there && key >= lo[n][e] && key < hi[n][e]))
-                                    S[blk][n][2 * u + e] = -CUDART_INF_F;
+                            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    mx[n][e] =
+                                        fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
+                                const float nm = fmaxf(m[n][e], mx[n][e]);
+                                const float f = nm == m[n][e] ? 1.f : ex2(m[n][e] - nm);
+                                m[n][e] = nm;
+                                // a row that has seen nothing: 2^(-inf) = 0 against any base
+                                base[n][e] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
+                                if constexpr (!APART) l[n][e] *= f;
+#pragma unroll
+                                for (int k = 0; k < NV / 2; ++k) {
+                                    O[k][n][e] *= f;
+                                    O[k][n][2 + e] *= f;
+                                }
+                            }
                     }
+                    // ---- weights and the second product
+#pragma unroll
+                    for (int blk = 0; blk < NBP; ++blk) {
+                        uint32_t p[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float w[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    w[e] = ex2(S[blk][n][2 * u + e] + base[n][e]);
+                                    if constexpr (!APART)
+                                        l[n][e] = __fmaf_rn(w[e], rsv[blk][u], l[n][e]);
+                                }
+                                p[n][u] = transpose8(f2_to_f16x2(w[0], w[1]));
+                            }
+                        const uint32_t r0 = st + St::kCodes + (16 * (b0 + blk) + t) * St::kRow;
+                        constexpr int VW = kKvWords<B, NV>;
+                        uint32_t v[4][VW];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            kv_lds_codes<B, NV>(r0 + 4 * k * St::kRow, g, v[k]);
+                        constexpr int P = NV < H ? NV : H;  // values of a half word
+                        static_for<0, NV / P>([&](auto hh) {
+                            constexpr int hw = decltype(hh)::value, w = hw / 2;
+                            constexpr uint32_t sel = hw & 1 ? 0x7632 : 0x5410;
+                            uint32_t a0[P], a2[P];
+                            kv_widen_f16<B, P>(__byte_perm(v[0][w], v[1][w], sel), a0);
+                            kv_widen_f16<B, P>(__byte_perm(v[2][w], v[3][w], sel), a2);
+#pragma unroll
+                            for (int i = 0; i < P; i += 2)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16(O[(P * hw + i) / 2][n], a0[i], a0[i + 1], a2[i],
+                                            a2[i + 1], p[n][0], p[n][1]);
+                        });
+                    }
+                }
+                __syncwarp();  // the stage is read
+                issue(it + St::kCount, next_page);
+                next_page = page_of(it + St::kCount + 1);
             }
+            // after a timeout: the copies still in flight, before their stages are reused
+            for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
+                mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
+                                nullptr);
+            done += steps;
+            return it < steps;
+        };
+        bool late = pass(ic_bool<false>{});
+        if (odd) sts32(odd_s, 1);
+        __syncthreads();  // (the rings are free as well)
+        bool apart = __builtin_expect(lds32(odd_s) != 0, 0);
+        if (apart) {  // unless they were zero scales alone
+            bool far = false;
+            for (int key = begin + threadIdx.x; key < end; key += kThreads) {
+                const int pi = (int)pl.div_page(key), page = kv_page(kb, c.num_pages, b, pi);
+                if (page >= 0)
+                    far |= !k12::folds(c.vs[((int64_t)page * c.heads + h) * c.page_size +
+                                            (key - pi * c.page_size)]);
+            }
+            apart = __syncthreads_or(far);
+            if (threadIdx.x == 0) sts32(odd_s, 0);
+        }
+        if (__builtin_expect(apart, 0)) {
+            if (!late) {
+                start();
+                late = pass(ic_bool<true>{});
+            }
+            // both sums against the point half way between theirs
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mx[n][e] = fmaxf(S[0][n][e], S[0][n][2 + e]);
+                    if (ref[n][e] == -CUDART_INF_F) continue;
+                    const float C = 0.5f * (m[n][e] + ref[n][e]), up = ex2(m[n][e] - C);
+                    l[n][e] *= ex2(ref[n][e] - C);
+                    m[n][e] = C;
 #pragma unroll
-                    for (int blk = 1; blk < NB; ++blk)
-                        mx[n][e] = max3(mx[n][e], S[blk][n][e], S[blk][n][2 + e]);
+                    for (int k = 0; k < NV / 2; ++k) {
+                        O[k][n][e] *= up;
+                        O[k][n][2 + e] *= up;
+                    }
                 }
-            // each lane looks at its own positions' largest; only when one is too far
-            // above the reference do the lanes of a row find their common one
-            bool far = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                far |= mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
-            if (__any_sync(0xffffffffu, far)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
-                        const float nm = fmaxf(m[n][e], mx[n][e]);
-                        const float f = nm == m[n][e] ? 1.f : ex2(m[n][e] - nm);
-                        m[n][e] = nm;
-                        // a row that has seen nothing: 2^(-inf) = 0 against any base
-                        base[n][e] = nm == -CUDART_INF_F ? 0.f : kShift - nm;
-                        l[n][e] *= f;
-#pragma unroll
-                        for (int k = 0; k < NV / 2; ++k) {
-                            O[k][n][e] *= f;
-                            O[k][n][2 + e] *= f;
-                        }
-                    }
-            }
-            // ---- weights and the second product
-#pragma unroll
-            for (int blk = 0; blk < NB; ++blk) {
-                uint32_t p[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float w[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            w[e] = ex2(S[blk][n][2 * u + e] + base[n][e]);
-                            l[n][e] = __fmaf_rn(w[e], rsv[blk][u], l[n][e]);
-                        }
-                        p[n][u] = transpose8(f2_to_f16x2(w[0], w[1]));
-                    }
-                const uint32_t r0 = st + St::kCodes + (16 * blk + t) * St::kRow;
-                constexpr int VW = kKvWords<B, NV>;
-                uint32_t v[4][VW];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) kv_lds_codes<B, NV>(r0 + 4 * k * St::kRow, g, v[k]);
-                constexpr int P = NV < H ? NV : H;  // values of a half word
-                static_for<0, NV / P>([&](auto hh) {
-                    constexpr int hw = decltype(hh)::value, w = hw / 2;
-                    constexpr uint32_t sel = hw & 1 ? 0x7632 : 0x5410;
-                    uint32_t a0[P], a2[P];
-                    kv_widen_f16<B, P>(__byte_perm(v[0][w], v[1][w], sel), a0);
-                    kv_widen_f16<B, P>(__byte_perm(v[2][w], v[3][w], sel), a2);
-#pragma unroll
-                    for (int i = 0; i < P; i += 2)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_f16(O[(P * hw + i) / 2][n], a0[i], a0[i + 1], a2[i], a2[i + 1],
-                                    p[n][0], p[n][1]);
-                });
-            }
-            __syncwarp();  // the stage is read
-            issue(it + St::kCount, next_page);
-            next_page = page_of(it + St::kCount + 1);
+            __syncthreads();
         }
-        // after a timeout: the copies still in flight, before their stages are reused
-        for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
-            mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
-                            nullptr);
-        done += steps;
-        const bool late = it < steps;
         // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -464,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
                     l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-        __syncthreads();  // the rings are free
         float* so = reinterpret_cast<float*>(smem);         // [warp][R][D + 4]
         float* sm = so + kWarps * R * (D + 4);              // [warp][R]: m, then l
         float* sl = sm + kWarps * R;

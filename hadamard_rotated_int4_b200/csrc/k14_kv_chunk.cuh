@@ -8,7 +8,9 @@
 // values against fp16 weights) and the scales cost one packed fma per pair of
 // scores.  The reference point m follows the running maximum only when a
 // score passes it by more than 2^8 (weights stay below 2^14 in fp16): the
-// accumulator in tensor memory is rescaled a few times a row, not every tile.
+// accumulator in tensor memory is rescaled a few times a row, not every tile.  Where V's
+// scales are too small or too large for 1 / sv, a CTA takes its positions once more and
+// sums the normaliser apart (k12_kv_attention.cuh).
 //
 // One CTA: one sequence, cached head and 2 x 128 head rows (128 at D = 256),
 // and a range of positions, widened in tiles of KT and worked on in parts of 64.
@@ -65,6 +67,7 @@ constexpr int kMmaWarp = 15;
 constexpr float kShift = 6.f;        // weights are held times 2^6 ...
 constexpr float kLazy = 8.f;         // ... and may pass the reference by 2^8
 constexpr int kScaleStages = 4;
+constexpr float kNowhere = -1e30f;   // in a scale's place: no position
 
 template <int D>
 struct Tile {
@@ -76,7 +79,7 @@ struct Tile {
     static constexpr int kQ = NQ * 128 * kPanels * 128;  // bytes
     static constexpr int kStage = KT * kPanels * 128;    // one operand tile
     static constexpr int kScale = KT * 12;               // (ck, ck, lv, lv) a pair, then 1/sv
-    static constexpr int kBars = 256;
+    static constexpr int kBars = 512;                    // two sets: one to a pass
     static constexpr int kUnits = KT * (D / 32) / 32;    // warp units of 32 x 32 codes
     static constexpr int kConv = 15 - 4 * NQ;            // widening warps
     static constexpr int kMine = (kUnits + kConv - 1) / kConv;
@@ -239,6 +242,61 @@ __host__ __device__ constexpr int place_of(int n) {
     return p / H * 2 * H + p % H + (n & 1) * H;
 }
 
+// What a CTA has to do: rows from row0 on of sequence b, over the positions of sp.
+template <int D>
+struct Task {
+    k12::Rows s;
+    k12::Split sp;
+    int b, row0, nr, parts, tiles, sets;  // sets: row sets that have rows
+    bool work;
+    // what all sets report is reported twice where one is missing
+    __device__ __forceinline__ void arrive_for_all(uint32_t bar) const {
+        for (int k = sets; k <= Tile<D>::NQ; ++k) mbar_arrive_one(bar);
+    }
+};
+template <int D>
+__device__ __forceinline__ Task<D> task_of(const Plan& pl, const KvCache& c, const KvBatch& kb,
+                                           const KvAttn& a, const volatile int* where, int split) {
+    using T = Tile<D>;
+    Task<D> k = {};
+    k.b = where[0];
+    k.row0 = where[1] * 128 * T::NQ;
+    if (k.b >= 0) {
+        k.s = k12::rows_of(kb, c.page_size, a, k.b);
+        k.nr = k.s.n * a.group;
+        k.sp = k12::split_of(
+            pl, k12::range_of(a, k.s, k.row0, min(k.nr, k.row0 + 128 * T::NQ) - 1), split);
+    }
+    k.work = k.b >= 0 && split < max(k.sp.count, 1);
+    k.parts = !k.work || k.sp.count == 0 ? 0 : (k.sp.end - k.sp.begin + 63) / 64;
+    k.tiles = (k.parts + T::kParts - 1) / T::kParts;
+    k.sets = !k.work ? 0 : T::NQ == 2 && k.nr - k.row0 > 128 ? 2 : 1;
+    return k;
+}
+
+// The barriers of one pass.
+struct Barriers {
+    uint32_t at;
+    __device__ __forceinline__ uint32_t kfull(int s) const { return at + 8u * s; }
+    __device__ __forceinline__ uint32_t kempty(int s) const { return at + 8u * (2 + s); }
+    __device__ __forceinline__ uint32_t vfull(int s) const { return at + 8u * (4 + s); }
+    __device__ __forceinline__ uint32_t vempty(int s) const { return at + 8u * (6 + s); }
+    __device__ __forceinline__ uint32_t scfull(int s) const { return at + 8u * (8 + s); }
+    __device__ __forceinline__ uint32_t scempty(int s) const { return at + 8u * (12 + s); }
+    // 2 * set + buffer
+    __device__ __forceinline__ uint32_t sfull(int s) const { return at + 8u * (16 + s); }
+    __device__ __forceinline__ uint32_t pfull(int s) const { return at + 8u * (20 + s); }
+    __device__ __forceinline__ uint32_t ofull(int set) const { return at + 8u * (24 + set); }
+    __device__ __forceinline__ uint32_t drain() const { return at + 8u * 27; }
+    static constexpr int kCount = 28;
+    template <int CONV, int NQ>
+    static __device__ __forceinline__ uint32_t arrivals(int i) {
+        if (i < 8) return (i & 2) == 0 ? CONV : 1;          // kfull, vfull; kempty, vempty
+        if (i >= 12 && i < 16) return 4 * NQ;                // scempty
+        return i >= 20 && i < 24 ? 4 : i == 26 ? 4 * NQ : 1;  // pfull; the queries'; the rest
+    }
+};
+
 template <int D, int B>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch kb, KvAttn a,
                                                             Plan pl, float* part,
@@ -255,16 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     uint8_t* bar_p = smem_base + (bar_s - base_s);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_p + 240);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_p + 244);
-    auto kfull = [&](int s) { return bar_s + 8u * s; };
-    auto kempty = [&](int s) { return bar_s + 8u * (2 + s); };
-    auto vfull = [&](int s) { return bar_s + 8u * (4 + s); };
-    auto vempty = [&](int s) { return bar_s + 8u * (6 + s); };
-    auto scfull = [&](int s) { return bar_s + 8u * (8 + s); };
-    auto scempty = [&](int s) { return bar_s + 8u * (12 + s); };
-    auto sfull = [&](int s) { return bar_s + 8u * (16 + s); };  // 2 * set + buffer
-    auto pfull = [&](int s) { return bar_s + 8u * (20 + s); };
-    auto ofull = [&](int set) { return bar_s + 8u * (24 + set); };
-    const uint32_t qfull = bar_s + 8u * 26, drain = bar_s + 8u * 27;
+    const uint32_t odd_s = bar_s + 256 + 240;  // a flag: V's scales need a second pass
+    const uint32_t qfull = bar_s + 8u * 26;
 
     // ---- which rows, which positions: all heads of one block, then those of the next
     const int split = (int)(blockIdx.x % pl.splits), nth = (int)(blockIdx.x / pl.splits);
@@ -278,27 +328,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
             where[1] = blk.rb;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int i = 0; i < 2; ++i) {
-                mbar_init_count(kfull(i), T::kConv);
-                mbar_init_count(kempty(i), 1);
-                mbar_init_count(vfull(i), T::kConv);
-                mbar_init_count(vempty(i), 1);
-                mbar_init_count(ofull(i), 1);
-            }
-            for (int i = 0; i < 4; ++i) {
-                mbar_init_count(sfull(i), 1);
-                mbar_init_count(pfull(i), 4);
-            }
-            for (int i = 0; i < kScaleStages; ++i) {
-                mbar_init_count(scfull(i), 1);
-                mbar_init_count(scempty(i), 4 * NQ);
-            }
-            mbar_init_count(qfull, 4 * NQ);
-            mbar_init_count(drain, 1);
-            *abort_flag = 0;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        // a lane to each barrier of a set (the queries' one, 26, is in the first alone)
+        if (lane < Barriers::kCount) {
+            const uint32_t n = Barriers::arrivals<T::kConv, NQ>(lane);
+            mbar_init_count(bar_s + 8 * lane, n);
+            mbar_init_count(bar_s + 256 + 8 * lane, n);
         }
+        if (lane == 0) {
+            sts32(odd_s, 0);
+            *abort_flag = 0;
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     } else if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(tmem_slot))
@@ -311,109 +351,52 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
     }
     __syncthreads();
     tmem_fence_after();
-    const int b = where[0], rb = where[1];
-    k12::Rows s = {};
-    k12::Split sp = {};
-    const int row0 = rb * 128 * NQ;
-    int nr = 0;
-    if (b >= 0) {
-        s = k12::rows_of(kb, c.page_size, a, b);
-        nr = s.n * a.group;
-        sp = k12::split_of(pl, k12::range_of(a, s, row0, min(nr, row0 + 128 * NQ) - 1), split);
-    }
-    const bool work = b >= 0 && split < max(sp.count, 1);
-    if (work) pdl_launch_dependents();
-    const int parts = !work || sp.count == 0 ? 0 : (sp.end - sp.begin + 63) / 64;
-    const int tiles = (parts + T::kParts - 1) / T::kParts;
-    // row sets that have rows; what they all report is reported twice where one is missing
-    const int sets = !work ? 0 : NQ == 2 && nr - row0 > 128 ? 2 : 1;
-    auto arrive_for_all = [&](uint32_t bar) {
-        for (int k = sets; k <= NQ; ++k) mbar_arrive_one(bar);
-    };
+    const Task<D> first = task_of<D>(pl, c, kb, a, where, split);
+    if (first.work) pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, status};
 
-    if (warp < 4 * NQ) {
-        // ================= softmax
-        reg_alloc<144>();
+    // A pass over the positions, by each role.  Where V's scales need the normaliser summed
+    // apart, which the warp that lays them out finds out, nothing is stored after the first
+    // pass, and a second one (APART) takes its time; the queries stay.
+    auto softmax = [&](auto apart, const Task<D>& task) {
+        constexpr bool APART = decltype(apart)::value;
+        const Barriers bar{bar_s + (APART ? 256u : 0u)};
+        const k12::Rows& s = task.s;
+        const k12::Split& sp = task.sp;
+        const int row0 = task.row0, nr = task.nr, parts = task.parts;
         const int set = warp >> 2, quarter = warp & 3, g = lane >> 2, t = lane & 3;
-        if (set < sets) {
-            // ---- this set's queries into the operand layout
-            const Lane<D> ql(lane);
-            const uint32_t qbase = q_s + set * 128 * T::kPanels * 128;
-            constexpr int kUnits = 128 / Lane<D>::kRows;
-            constexpr int kLoads = kUnits >= 16 ? 4 : kUnits / 4;  // units in flight
-#pragma unroll 1
-            for (int u0 = quarter; u0 < kUnits; u0 += 4 * kLoads) {
-                uint32_t raw[kLoads][16];
+        // ---- rows of this thread: 16 hf + 8 u + g of the warp's 32
+        int lo[4], hi[4];
+        int max_lo = 0, min_hi = 0x7fffffff;
 #pragma unroll
-                for (int v = 0; v < kLoads; ++v) {
-                    const int u = u0 + 4 * v, row = u * Lane<D>::kRows + ql.row;
-                    const int r = row0 + set * 128 + row, i = r / a.group;
-                    const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
-                                          (int64_t)(h * a.group + (r - i * a.group)) * a.q_head +
-                                          ql.group * 32;
+        for (int k = 0; k < 4; ++k) {
+            const int r = min(row0 + set * 128 + 32 * quarter + 8 * k + g, nr - 1);
+            const int p = s.first + r / a.group;
+            hi[k] = a.causal ? p + 1 : 0x7fffffff;
+            lo[k] = k12::window_begin(a, p);
+            max_lo = max(max_lo, lo[k]);
+            min_hi = min(min_hi, hi[k]);
+        }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 z = r < nr
-                                            ? reinterpret_cast<const uint4*>(src)[k]
-                                            : make_uint4(0, 0, 0, 0);
-                        raw[v][4 * k] = z.x;
-                        raw[v][4 * k + 1] = z.y;
-                        raw[v][4 * k + 2] = z.z;
-                        raw[v][4 * k + 3] = z.w;
-                    }
-                }
+        for (int o = 4; o < 32; o <<= 1) {
+            max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
+            min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
+        }
+        float m[4], base[4], ref[4];  // (ref: what l counts against, APART)
+        float2 l[4];
 #pragma unroll
-                for (int v = 0; v < kLoads; ++v) {
-                    const int u = u0 + 4 * v;
-                    uint32_t out[16];
-                    static_for<0, 16>([&](auto pp) {
-                        constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
-                        constexpr int e1 = place_of<B>(2 * decltype(pp)::value + 1);
-                        out[decltype(pp)::value] =
-                            __byte_perm(raw[v][e0 / 2], raw[v][e1 / 2],
-                                        (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
-                    });
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sts128(qbase + chunk_at(128, u * Lane<D>::kRows + ql.row, ql.group, k),
-                               make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2],
-                                          out[4 * k + 3]));
-                }
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) arrive_for_all(qfull);
-
-            // ---- rows of this thread: 16 hf + 8 u + g of the warp's 32
-            int lo[4], hi[4];
-            int max_lo = 0, min_hi = 0x7fffffff;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = min(row0 + set * 128 + 32 * quarter + 8 * k + g, nr - 1);
-                const int p = s.first + r / a.group;
-                hi[k] = a.causal ? p + 1 : 0x7fffffff;
-                lo[k] = k12::window_begin(a, p);
-                max_lo = max(max_lo, lo[k]);
-                min_hi = min(min_hi, hi[k]);
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
-                min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
-            }
-            float m[4], base[4];
-            float2 l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                m[k] = -CUDART_INF_F;
-                base[k] = 0.f;
-                l[k] = make_float2(0.f, 0.f);
-            }
-            const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-            const uint32_t o_t = tmem + lanes + T::kOCol + set * D;
-            bool ok = true;
+        for (int k = 0; k < 4; ++k) {
+            m[k] = -CUDART_INF_F;
+            base[k] = 0.f;
+            ref[k] = -CUDART_INF_F;
+            l[k] = make_float2(0.f, 0.f);
+        }
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t o_t = tmem + lanes + T::kOCol + set * D;
+        // ---- the parts, APART: in the same steps, two references to a row
+        bool ok = true;
+        if constexpr (!APART) {
 #pragma unroll 1
             for (int i = 0; i < parts; ++i) {
                 const int sb = 2 * set + (i & 1), j = i / T::kParts;
@@ -426,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                     reinterpret_cast<const float4*>(sc_p + (i % T::kParts) * 512) + t;
                 const float2* const rs2 =
                     reinterpret_cast<const float2*>(sc_p + KT * 8 + (i % T::kParts) * 256) + t;
-                ok = wait.all(scfull(j % kScaleStages), (j / kScaleStages) & 1) &&
-                     wait.all(sfull(sb), (i >> 1) & 1);
+                ok = wait.all(bar.scfull(j % kScaleStages), (j / kScaleStages) & 1) &&
+                     wait.all(bar.sfull(sb), (i >> 1) & 1);
                 if (!ok) break;
                 tmem_fence_after();
                 float x[2][32];
@@ -488,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                         l[r] = __fmul2_rn(l[r], make_float2(f[r], f[r]));
                     }
                     if (i > 0) {  // the accumulator, once the product before has landed
-                        ok = wait.all(ofull(set), (i - 1) & 1);
+                        ok = wait.all(bar.ofull(set), (i - 1) & 1);
                         if (!ok) break;
                         tmem_fence_after();
 #pragma unroll 1
@@ -528,336 +511,555 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive_one(pfull(sb));
+                    mbar_arrive_one(bar.pfull(sb));
                     if (i % T::kParts == T::kParts - 1 || i + 1 == parts)
-                        arrive_for_all(scempty(j % kScaleStages));
+                        task.arrive_for_all(bar.scempty(j % kScaleStages));
                 }
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float z = l[r].x + l[r].y;
-                z += __shfl_xor_sync(0xffffffffu, z, 1);
-                z += __shfl_xor_sync(0xffffffffu, z, 2);
-                l[r].x = z;
-            }
-            // ---- the accumulator out, a lane to a row, 32 columns at a time.  Every product
-            // has landed with the drain's single phase (a set's last product alone could not
-            // be told from the one before the one before it by a parity).
-            if (ok && parts > 0) ok = wait.all(drain, 0);
-            if (ok) {
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < parts; ++i) {
+                const int sb = 2 * set + (i & 1), j = i / T::kParts;
+                const uint32_t s_t = tmem + lanes + sb * 64;
+                const float4* const sc4 =
+                    reinterpret_cast<const float4*>(smem_base + (sc_s - base_s) +
+                                                    (j % kScaleStages) * T::kScale +
+                                                    (i % T::kParts) * 512) + t;
+                ok = wait.all(bar.scfull(j % kScaleStages), (j / kScaleStages) & 1) &&
+                     wait.all(bar.sfull(sb), (i >> 1) & 1) &&
+                     (i == 0 || wait.all(bar.ofull(set), (i - 1) & 1));
+                if (!ok) break;
                 tmem_fence_after();
-                // row 8k + g's sum and reference sit in lane 4g
-                float L = 0.f, M = 0.f;
+                const int key0 = sp.begin + i * 64;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {  // 16 rows at a time: registers before speed
+                    const uint32_t half = (uint32_t)(16 * hf) << 16;
+                    float x[32];
+                    tmem_ld_16x256b_x8(s_t + half, x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {  // scores; -inf where nothing is or may be seen
+                        const float4 f = sc4[4 * k];
+                        const int key = key0 + 8 * k + 2 * t;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 2 * hf + e / 2, at = key + (e & 1);
+                            const bool there = (e & 1 ? f.w : f.z) != kNowhere;
+                            x[4 * k + e] = there && at >= lo[r] && at < hi[r]
+                                               ? x[4 * k + e] * (e & 1 ? f.y : f.x)
+                                               : -CUDART_INF_F;
+                        }
+                    }
+                    float f2[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {  // their largest and sum
+                        const int r = 2 * hf + u;
+                        float top = -CUDART_INF_F;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            top = max3(top, x[4 * k + 2 * u], x[4 * k + 2 * u + 1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const float to = fmaxf(ref[r], top);
+                        if (to != ref[r]) l[r].x *= ex2(ref[r] - to);
+                        ref[r] = to;
+                        const float rb = to == -CUDART_INF_F ? 0.f : kShift - to;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            l[r].x += ex2(x[4 * k + 2 * u] + rb) + ex2(x[4 * k + 2 * u + 1] + rb);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {  // V's scales
+                        const float4 f = sc4[4 * k];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[4 * k + e] += e & 1 ? f.w : f.z;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int r = 2 * hf + u;
+                        float top = m[r];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            top = max3(top, x[4 * k + 2 * u], x[4 * k + 2 * u + 1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        f2[u] = top == m[r] ? 1.f : ex2(m[r] - top);
+                        m[r] = top;
+                        base[r] = top == -CUDART_INF_F ? 0.f : kShift - top;
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float to = base[2 * hf + u];
+                            p[2 * k + u] = f2_to_f16x2(ex2(x[4 * k + 2 * u] + to),
+                                                       ex2(x[4 * k + 2 * u + 1] + to));
+                        }
+                    tmem_st_16x128b_x8(s_t + half, p);
+                    if (i > 0) {
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            float o[16];
+                            tmem_ld_16x256b_x4(o_t + half + 32 * cc, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f2[e % 4 / 2];
+                            tmem_st_16x256b_x4(o_t + half + 32 * cc, o);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_one(bar.pfull(sb));
+                    if (i % T::kParts == T::kParts - 1 || i + 1 == parts)
+                        task.arrive_for_all(bar.scempty(j % kScaleStages));
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float z = l[r].x + l[r].y;
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            l[r].x = z;
+        }
+        // ---- the accumulator out, a lane to a row, 32 columns at a time.  Every product
+        // has landed with the drain's single phase (a set's last product alone could not
+        // be told from the one before the one before it by a parity).
+        if (ok && parts > 0) ok = wait.all(bar.drain(), 0);
+        // (the flag stands since the last part's scales, which this warp has waited for)
+        if (ok && (APART || lds32(odd_s) == 0)) {
+            tmem_fence_after();
+            // row 8k + g's sum and reference sit in lane 4g
+            float L = 0.f, M = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float lk = __shfl_sync(0xffffffffu, l[k].x, 4 * (lane & 7));
+                const float mk = __shfl_sync(0xffffffffu, m[k], 4 * (lane & 7));
+                if (lane >> 3 == k) {
+                    L = lk;
+                    M = mk - kShift;
+                }
+            }
+            float up = 1.f;
+            if constexpr (APART) {  // both sums against the point half way between theirs
+                float R = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float lk = __shfl_sync(0xffffffffu, l[k].x, 4 * (lane & 7));
-                    const float mk = __shfl_sync(0xffffffffu, m[k], 4 * (lane & 7));
-                    if (lane >> 3 == k) {
-                        L = lk;
-                        M = mk - kShift;
-                    }
+                    const float rk = __shfl_sync(0xffffffffu, ref[k], 4 * (lane & 7));
+                    if (lane >> 3 == k) R = rk - kShift;
                 }
-                const int row = row0 + set * 128 + 32 * quarter + lane;
-                const bool there = row < nr, whole = sp.count <= 1;
-                float inv = 1.f;
-                uint8_t* dst;
-                if (whole) {
-                    dst = reinterpret_cast<uint8_t*>(
-                        k12::row_out(a, s, h, row, M, L, there, &inv));
-                } else {
-                    const int i = row / a.group;
-                    float* to = part + k12::part_index(kb, a, split, s.row0 + i,
-                                                       h * a.group + row - i * a.group) *
-                                           (D + 4);
-                    if (there) *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
-                    dst = reinterpret_cast<uint8_t*>(to);
-                }
-                // Two neighbouring lanes store 32 bytes of one's row, then of the other's:
-                // whole sectors.  even and odd: those rows, from this lane's 16 bytes on.
-                const bool is_odd = lane & 1;
-                const uint64_t mine = reinterpret_cast<uint64_t>(dst);
-                const uint64_t next = __shfl_xor_sync(0xffffffffu, mine, 1);
-                const bool next_there = __shfl_xor_sync(0xffffffffu, (int)there, 1) != 0;
-                uint8_t* const even =
-                    reinterpret_cast<uint8_t*>(is_odd ? next : mine) + 16 * (lane & 1);
-                uint8_t* const odd =
-                    reinterpret_cast<uint8_t*>(is_odd ? mine : next) + 16 * (lane & 1);
-                const bool even_there = is_odd ? next_there : there;
-                const bool odd_there = is_odd ? there : next_there;
-                auto store_pair = [&](const uint32_t* lo, const uint32_t* hi, int at) {
-                    uint32_t e[4], o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t got =
-                            __shfl_xor_sync(0xffffffffu, is_odd ? lo[k] : hi[k], 1);
-                        e[k] = is_odd ? got : lo[k];
-                        o[k] = is_odd ? hi[k] : got;
-                    }
-                    if (even_there)
-                        *reinterpret_cast<uint4*>(even + at) = make_uint4(e[0], e[1], e[2], e[3]);
-                    if (odd_there)
-                        *reinterpret_cast<uint4*>(odd + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                };
-#pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {
-                    float o[32];
-                    if (parts > 0) {
-                        tmem_ld_32x32b_x32(o_t + 32 * cc, o);
-                        tmem_wait_ld(o);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                    }
-                    float y[32];  // back in the order of D
-                    static_for<0, 32>([&](auto n) {
-                        y[place_of<B>(decltype(n)::value)] = o[decltype(n)::value] * inv;
-                    });
-                    if (whole) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = f2_to_bf16x2(y[2 * e], y[2 * e + 1]);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            store_pair(w + 8 * q, w + 8 * q + 4, 64 * cc + 32 * q);
-                    } else {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(y[e]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            store_pair(w + 8 * q, w + 8 * q + 4, 128 * cc + 32 * q);
-                    }
+                if (R != -CUDART_INF_F) {
+                    const float C = 0.5f * (M + R);
+                    up = ex2(M - C);
+                    L *= ex2(R - C);
+                    M = C;
                 }
             }
+            const int row = row0 + set * 128 + 32 * quarter + lane;
+            const bool there = row < nr, whole = sp.count <= 1;
+            float inv = 1.f;
+            uint8_t* dst;
+            if (whole) {
+                dst = reinterpret_cast<uint8_t*>(
+                    k12::row_out(a, s, h, row, M, L, there, &inv));
+            } else {
+                const int i = row / a.group;
+                float* to = part + k12::part_index(kb, a, split, s.row0 + i,
+                                                   h * a.group + row - i * a.group) *
+                                       (D + 4);
+                if (there) *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
+                dst = reinterpret_cast<uint8_t*>(to);
+            }
+            // Two neighbouring lanes store 32 bytes of one's row, then of the other's:
+            // whole sectors.  even and odd: those rows, from this lane's 16 bytes on.
+            const bool is_odd = lane & 1;
+            const uint64_t mine = reinterpret_cast<uint64_t>(dst);
+            const uint64_t next = __shfl_xor_sync(0xffffffffu, mine, 1);
+            const bool next_there = __shfl_xor_sync(0xffffffffu, (int)there, 1) != 0;
+            uint8_t* const even =
+                reinterpret_cast<uint8_t*>(is_odd ? next : mine) + 16 * (lane & 1);
+            uint8_t* const odd =
+                reinterpret_cast<uint8_t*>(is_odd ? mine : next) + 16 * (lane & 1);
+            const bool even_there = is_odd ? next_there : there;
+            const bool odd_there = is_odd ? there : next_there;
+            auto store_pair = [&](const uint32_t* lo, const uint32_t* hi, int at) {
+                uint32_t e[4], o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t got =
+                        __shfl_xor_sync(0xffffffffu, is_odd ? lo[k] : hi[k], 1);
+                    e[k] = is_odd ? got : lo[k];
+                    o[k] = is_odd ? hi[k] : got;
+                }
+                if (even_there)
+                    *reinterpret_cast<uint4*>(even + at) = make_uint4(e[0], e[1], e[2], e[3]);
+                if (odd_there)
+                    *reinterpret_cast<uint4*>(odd + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            };
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+                float o[32];
+                if (parts > 0) {
+                    tmem_ld_32x32b_x32(o_t + 32 * cc, o);
+                    tmem_wait_ld(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                float y[32];  // back in the order of D
+                static_for<0, 32>([&](auto n) {
+                    const float v = o[decltype(n)::value];
+                    y[place_of<B>(decltype(n)::value)] = APART ? v * up * inv : v * inv;
+                });
+                if (whole) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = f2_to_bf16x2(y[2 * e], y[2 * e + 1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        store_pair(w + 8 * q, w + 8 * q + 4, 64 * cc + 32 * q);
+                } else {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(y[e]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        store_pair(w + 8 * q, w + 8 * q + 4, 128 * cc + 32 * q);
+                }
+            }
+        }
+    };
+    auto issue = [&](auto apart, const Task<D>& task) {
+        const int parts = task.parts, sets = task.sets;
+        const Barriers bar{bar_s + (decltype(apart)::value ? 256u : 0u)};
+        if (parts > 0) {
+            constexpr uint32_t kIdQk = idesc(true, false, 64), kIdPv = idesc(false, true, D);
+            constexpr uint32_t kPanel = KT * 128;
+            const uint64_t q_d = desc_k(q_s), k_d = desc_k(k_s), v_d = desc_v(v_s, kPanel);
+            // bytes to descriptor units
+            auto units = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
+            // scores of part i (64 rows of its tile's keys, score buffer i & 1) for both
+            // sets; a tile's keys are done with its last part
+            auto scores = [&](int i) {
+                const int j = i / T::kParts;
+                if (i % T::kParts == 0 && !wait.all(bar.kfull(j & 1), (j >> 1) & 1)) return false;
+                tmem_fence_after();
+                const uint64_t b0 = k_d + units((uint32_t)(j & 1) * T::kStage +
+                                                (uint32_t)(i % T::kParts) * 8192);
+                for (int set = 0; set < sets; ++set) {
+                    const uint32_t sb = (uint32_t)(2 * set + (i & 1));
+                    const uint64_t a0 = q_d + units((uint32_t)set * 128 * T::kPanels * 128);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + sb * 64, a0 + units((k / 4) * 128 * 128) + 2 * (k % 4),
+                               b0 + units((k / 4) * kPanel) + 2 * (k % 4), kIdQk, k != 0);
+                    commit(bar.sfull(sb));
+                }
+                if (i % T::kParts == T::kParts - 1) commit(bar.kempty(j & 1));
+                return true;
+            };
+            bool ok = wait.all(qfull, 0) && scores(0);
+            for (int i = 0; i < parts && ok; ++i) {
+                // part i + 1's buffer held the weights of part i - 1, whose product was
+                // issued before
+                if (i + 1 < parts) ok = scores(i + 1);
+                const int j = i / T::kParts;
+                if (ok && i % T::kParts == 0) ok = wait.all(bar.vfull(j & 1), (j >> 1) & 1);
+                const uint64_t b0 = v_d + units((uint32_t)(j & 1) * T::kStage +
+                                                (uint32_t)(i % T::kParts) * 8192);
+                for (int set = 0; set < sets && ok; ++set) {
+                    const uint32_t sb = (uint32_t)(2 * set + (i & 1));
+                    ok = wait.all(bar.pfull(sb), (i >> 1) & 1);
+                    if (!ok) break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tmem + T::kOCol + set * D, tmem + sb * 64 + 8 * k,
+                               b0 + units(k * 2048), kIdPv, i != 0 || k != 0);
+                    commit(bar.ofull(set));
+                }
+                if (ok && i % T::kParts == T::kParts - 1) commit(bar.vempty(j & 1));
+            }
+            // every MMA issued has completed once this commit arrives
+            commit(bar.drain());
+            if (!mbar_wait_clock(bar.drain(), 0, nullptr)) {
+                if (lane == 0) report_status(status, HBL_ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+        }
+    };
+    auto widen = [&](auto apart, const Task<D>& task) {
+        constexpr bool APART = decltype(apart)::value;
+        const Barriers bar{bar_s + (APART ? 256u : 0u)};
+        const k12::Split& sp = task.sp;
+        const int b = task.b, tiles = task.tiles;
+        const int cw = warp >= 8 ? warp - 8 : warp + 3;  // warps 8 .. 14, then 4 .. 7
+        const Lane<D> ln(lane);
+        uint32_t raw[2][T::kMine][B];  // keys, values: loaded a tile ahead
+        int page[2][T::kMine];  // of the units that are loaded next: keys, values
+        // this warp's i-th unit of a tile of K (values: dealt out from where the keys'
+        // left off, so that all get about the same)
+        constexpr int kConv = T::kConv, kTurn = kConv - T::kUnits % kConv;
+        auto unit = [&](bool val, int i) { return (val ? (cw + kTurn) % kConv : cw) + kConv * i; };
+        auto key_of = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
+            return sp.begin + (phase >> 1) * KT + unit(phase & 1, i) * Lane<D>::kRows + ln.row;
+        };
+        auto load_page = [&](int phase, int i) {
+            const int key = key_of(phase, i);
+            page[phase & 1][i] = unit(phase & 1, i) < T::kUnits && key < sp.end
+                                     ? kv_page(kb, c.num_pages, b, (int)pl.div_page(key))
+                                     : -1;
+        };
+        // the codes of a unit, whose page was looked up a tile ago
+        auto load = [&](int phase, int i) {
+            uint32_t(&to)[B] = raw[phase & 1][i];
+            const int key = key_of(phase, i), pg = page[phase & 1][i];
+            if (pg >= 0) {
+                const int64_t row = ((int64_t)pg * c.heads + h) * c.page_size +
+                                    (key - (int)pl.div_page(key) * c.page_size);
+                const uint8_t* src = ((phase & 1) ? c.vc : c.kc) + row * ROW_BYTES +
+                                     ln.group * (4 * B);
+                if constexpr (B % 4 == 0) {
+#pragma unroll
+                    for (int k = 0; k < B / 4; ++k) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
+                        to[4 * k] = v.x;
+                        to[4 * k + 1] = v.y;
+                        to[4 * k + 2] = v.z;
+                        to[4 * k + 3] = v.w;
+                    }
+                } else if constexpr (B == 2) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+                    to[0] = v.x;
+                    to[1] = v.y;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < B; ++k)
+                        to[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+                }
+            } else {  // nothing there: any finite codes (their weight is zero)
+#pragma unroll
+                for (int k = 0; k < B; ++k) to[k] = 0;
+            }
+            load_page(phase + 2, i);
+        };
+        uint32_t lane_at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lane_at[k] = chunk_at(KT, ln.row, ln.group, k);
+        auto store = [&](auto bf16, int i, int u, uint32_t dst) {
+            uint32_t out[16];
+            widen32<B, decltype(bf16)::value>(raw[decltype(bf16)::value ? 0 : 1][i], out);
+            // (row & 7, which the swizzle goes by, is the lane's own where a unit
+            // has a multiple of eight rows, and flips bit 2 in odd units of four)
+            const uint32_t to = dst + u * Lane<D>::kRows * 128;
+            const uint32_t flip = Lane<D>::kRows % 8 == 0 ? 0u : (uint32_t)(u & 1) << 6;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sts128(to + (lane_at[k] ^ flip),
+                       make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
+        };
+        const float xscale = a.scale * 1.4426950408889634f;
+        // scales of a tile: four positions a lane, by the last widening warp, which
+        // looks up their page a tile before
+        float4 sk, sv;
+        bool sc_there = false;
+        int sc_page = -2;
+        auto load_scales_page = [&](int j) {
+            const int key = sp.begin + j * KT + 4 * lane;
+            if (4 * lane < KT && key < sp.end) {
+                sc_page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
+            } else {
+                sc_page = -2;  // no position; -1: no such page
+            }
+        };
+        auto load_scales = [&](int j) {
+            const int key = sp.begin + j * KT + 4 * lane;
+            sc_there = sc_page >= 0;
+            if (sc_page == -1) report_status(status, HBL_ERR_INVALID_ARG);
+            if (sc_there) {
+                const int64_t row = ((int64_t)sc_page * c.heads + h) * c.page_size +
+                                    (key - (int)pl.div_page(key) * c.page_size);
+                sk = *reinterpret_cast<const float4*>(c.ks + row);
+                sv = *reinterpret_cast<const float4*>(c.vs + row);
+            }
+            load_scales_page(j + 1);
+        };
+        auto store_scales = [&](int j) {
+            if (4 * lane >= KT) return;
+            const uint32_t sc = sc_s + (j % kScaleStages) * T::kScale;
+            const int key = sp.begin + j * KT + 4 * lane;
+            const float k4[4] = {sk.x, sk.y, sk.z, sk.w}, v4[4] = {sv.x, sv.y, sv.z, sv.w};
+            float ck[4], lv[4], rs[4];
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // a position that is not there: 0 * x - inf
+                const bool there = sc_there && key + e < sp.end;
+                ck[e] = there ? __fmul_rn(k4[e], xscale) : 0.f;
+                if constexpr (APART) {
+                    lv[e] = there ? fmaxf(k12::lg2_any(v4[e]), k12::kNoScale) : kNowhere;
+                    rs[e] = 0.f;  // (not used)
+                } else {
+                    lv[e] = there ? fmaxf(lg2(v4[e]), k12::kZeroFold) : -CUDART_INF_F;
+                    rs[e] = there ? ex2(-lv[e]) : 0.f;
+                    odd |= there && !k12::folds(v4[e]);
+                }
+            }
+            if (odd) sts32(odd_s, 1);
+            auto f = [](float v) { return __float_as_uint(v); };
+            sts128(sc + lane * 32, make_uint4(f(ck[0]), f(ck[1]), f(lv[0]), f(lv[1])));
+            sts128(sc + lane * 32 + 16, make_uint4(f(ck[2]), f(ck[3]), f(lv[2]), f(lv[3])));
+            sts128(sc + KT * 8 + lane * 16, make_uint4(f(rs[0]), f(rs[1]), f(rs[2]), f(rs[3])));
+        };
+        const bool scales = cw == kConv - 1;
+        if (scales) {
+            load_scales_page(0);
+            load_scales(0);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kMine; ++i) {
+            load_page(0, i);
+            load_page(1, i);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kMine; ++i) load(0, i);
+#pragma unroll
+        for (int i = 0; i < T::kMine; ++i) load(1, i);
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < tiles && ok; ++j) {
+            const int st = j & 1;
+            const uint32_t par = ((j >> 1) & 1) ^ 1;
+            if (scales) {
+                if (j >= kScaleStages)
+                    ok = wait.all(bar.scempty(j % kScaleStages), ((j / kScaleStages) & 1) ^ 1);
+                if (!ok) break;
+                store_scales(j);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(bar.scfull(j % kScaleStages));
+                load_scales(j + 1);
+            }
+            if (j >= 2) ok = wait.all(bar.kempty(st), par);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < T::kMine; ++i) {
+                const int u = unit(false, i);
+                if (u < T::kUnits) store(ic_bool<true>{}, i, u, k_s + st * T::kStage);
+                load(2 * j + 2, i);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(bar.kfull(st));
+            if (j >= 2) ok = wait.all(bar.vempty(st), par);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < T::kMine; ++i) {
+                const int u = unit(true, i);
+                if (u < T::kUnits) store(ic_bool<false>{}, i, u, v_s + st * T::kStage);
+                load(2 * j + 3, i);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(bar.vfull(st));
+        }
+    };
+    // behind a pass: what tensor memory holds is read; all roles know of a second one
+    auto done = [&] {
+        __syncwarp();
+        tmem_fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");
+        tmem_fence_after();
+    };
+    auto again = [&] {
+        done();
+        return lds32(odd_s) != 0 && *abort_flag == 0;
+    };
+    if (warp < 4 * NQ) {
+        // ================= softmax
+        reg_alloc<144>();
+        const int set = warp >> 2, quarter = warp & 3;
+        if (set < first.sets) {
+            const k12::Rows& s = first.s;
+            const int row0 = first.row0, nr = first.nr;
+            // ---- this set's queries into the operand layout
+            const Lane<D> ql(lane);
+            const uint32_t qbase = q_s + set * 128 * T::kPanels * 128;
+            constexpr int kUnits = 128 / Lane<D>::kRows;
+            constexpr int kLoads = kUnits >= 16 ? 4 : kUnits / 4;  // units in flight
+#pragma unroll 1
+            for (int u0 = quarter; u0 < kUnits; u0 += 4 * kLoads) {
+                uint32_t raw[kLoads][16];
+#pragma unroll
+                for (int v = 0; v < kLoads; ++v) {
+                    const int u = u0 + 4 * v, row = u * Lane<D>::kRows + ql.row;
+                    const int r = row0 + set * 128 + row, i = r / a.group;
+                    const uint16_t* src = a.q + (int64_t)(s.row0 + i) * a.q_row +
+                                          (int64_t)(h * a.group + (r - i * a.group)) * a.q_head +
+                                          ql.group * 32;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 z = r < nr
+                                            ? reinterpret_cast<const uint4*>(src)[k]
+                                            : make_uint4(0, 0, 0, 0);
+                        raw[v][4 * k] = z.x;
+                        raw[v][4 * k + 1] = z.y;
+                        raw[v][4 * k + 2] = z.z;
+                        raw[v][4 * k + 3] = z.w;
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < kLoads; ++v) {
+                    const int u = u0 + 4 * v;
+                    uint32_t out[16];
+                    static_for<0, 16>([&](auto pp) {
+                        constexpr int e0 = place_of<B>(2 * decltype(pp)::value);
+                        constexpr int e1 = place_of<B>(2 * decltype(pp)::value + 1);
+                        out[decltype(pp)::value] =
+                            __byte_perm(raw[v][e0 / 2], raw[v][e1 / 2],
+                                        (e0 & 1 ? 0x32 : 0x10) | (e1 & 1 ? 0x7600 : 0x5400));
+                    });
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts128(qbase + chunk_at(128, u * Lane<D>::kRows + ql.row, ql.group, k),
+                               make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2],
+                                          out[4 * k + 3]));
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) first.arrive_for_all(qfull);
+
+            softmax(ic_bool<false>{}, first);
+        }
+        if (again()) {
+            const Task<D> task = task_of<D>(pl, c, kb, a, where, split);
+            if (set < task.sets) softmax(ic_bool<true>{}, task);
+            done();
         }
     } else {
         if (warp >= 8) reg_dealloc<112>();  // (warps 4 .. 7 keep what they have)
         if (warp == kMmaWarp) {
             // ================= MMA issue
-            if (parts > 0) {
-                constexpr uint32_t kIdQk = idesc(true, false, 64), kIdPv = idesc(false, true, D);
-                constexpr uint32_t kPanel = KT * 128;
-                const uint64_t q_d = desc_k(q_s), k_d = desc_k(k_s), v_d = desc_v(v_s, kPanel);
-                // bytes to descriptor units
-                auto units = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
-                // scores of part i (64 rows of its tile's keys, score buffer i & 1) for both
-                // sets; a tile's keys are done with its last part
-                auto scores = [&](int i) {
-                    const int j = i / T::kParts;
-                    if (i % T::kParts == 0 && !wait.all(kfull(j & 1), (j >> 1) & 1)) return false;
-                    tmem_fence_after();
-                    const uint64_t b0 = k_d + units((uint32_t)(j & 1) * T::kStage +
-                                                    (uint32_t)(i % T::kParts) * 8192);
-                    for (int set = 0; set < sets; ++set) {
-                        const uint32_t sb = (uint32_t)(2 * set + (i & 1));
-                        const uint64_t a0 = q_d + units((uint32_t)set * 128 * T::kPanels * 128);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_ss(tmem + sb * 64, a0 + units((k / 4) * 128 * 128) + 2 * (k % 4),
-                                   b0 + units((k / 4) * kPanel) + 2 * (k % 4), kIdQk, k != 0);
-                        commit(sfull(sb));
-                    }
-                    if (i % T::kParts == T::kParts - 1) commit(kempty(j & 1));
-                    return true;
-                };
-                bool ok = wait.all(qfull, 0) && scores(0);
-                for (int i = 0; i < parts && ok; ++i) {
-                    // part i + 1's buffer held the weights of part i - 1, whose product was
-                    // issued before
-                    if (i + 1 < parts) ok = scores(i + 1);
-                    const int j = i / T::kParts;
-                    if (ok && i % T::kParts == 0) ok = wait.all(vfull(j & 1), (j >> 1) & 1);
-                    const uint64_t b0 = v_d + units((uint32_t)(j & 1) * T::kStage +
-                                                    (uint32_t)(i % T::kParts) * 8192);
-                    for (int set = 0; set < sets && ok; ++set) {
-                        const uint32_t sb = (uint32_t)(2 * set + (i & 1));
-                        ok = wait.all(pfull(sb), (i >> 1) & 1);
-                        if (!ok) break;
-                        tmem_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ts(tmem + T::kOCol + set * D, tmem + sb * 64 + 8 * k,
-                                   b0 + units(k * 2048), kIdPv, i != 0 || k != 0);
-                        commit(ofull(set));
-                    }
-                    if (ok && i % T::kParts == T::kParts - 1) commit(vempty(j & 1));
-                }
-                // every MMA issued has completed once this commit arrives
-                commit(drain);
-                if (!mbar_wait_clock(drain, 0, nullptr) && lane == 0)
-                    report_status(status, HBL_ERR_TIMEOUT);
+            issue(ic_bool<false>{}, first);
+            if (again()) {
+                issue(ic_bool<true>{}, task_of<D>(pl, c, kb, a, where, split));
+                done();
             }
-        } else if (tiles > 0) {
+        } else {
             // ================= widening
-            const int cw = warp >= 8 ? warp - 8 : warp + 3;  // warps 8 .. 14, then 4 .. 7
-            const Lane<D> ln(lane);
-            uint32_t raw[2][T::kMine][B];  // keys, values: loaded a tile ahead
-            int page[2][T::kMine];  // of the units that are loaded next: keys, values
-            // this warp's i-th unit of a tile of K (values: dealt out from where the keys'
-            // left off, so that all get about the same)
-            constexpr int kConv = T::kConv, kTurn = kConv - T::kUnits % kConv;
-            auto unit = [&](bool val, int i) { return (val ? (cw + kTurn) % kConv : cw) + kConv * i; };
-            auto key_of = [&](int phase, int i) {  // phase 2j: keys of tile j, 2j + 1: values
-                return sp.begin + (phase >> 1) * KT + unit(phase & 1, i) * Lane<D>::kRows + ln.row;
-            };
-            auto load_page = [&](int phase, int i) {
-                const int key = key_of(phase, i);
-                page[phase & 1][i] = unit(phase & 1, i) < T::kUnits && key < sp.end
-                                         ? kv_page(kb, c.num_pages, b, (int)pl.div_page(key))
-                                         : -1;
-            };
-            // the codes of a unit, whose page was looked up a tile ago
-            auto load = [&](int phase, int i) {
-                uint32_t(&to)[B] = raw[phase & 1][i];
-                const int key = key_of(phase, i), pg = page[phase & 1][i];
-                if (pg >= 0) {
-                    const int64_t row = ((int64_t)pg * c.heads + h) * c.page_size +
-                                        (key - (int)pl.div_page(key) * c.page_size);
-                    const uint8_t* src = ((phase & 1) ? c.vc : c.kc) + row * ROW_BYTES +
-                                         ln.group * (4 * B);
-                    if constexpr (B % 4 == 0) {
-#pragma unroll
-                        for (int k = 0; k < B / 4; ++k) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
-                            to[4 * k] = v.x;
-                            to[4 * k + 1] = v.y;
-                            to[4 * k + 2] = v.z;
-                            to[4 * k + 3] = v.w;
-                        }
-                    } else if constexpr (B == 2) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-                        to[0] = v.x;
-                        to[1] = v.y;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < B; ++k)
-                            to[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
-                    }
-                } else {  // nothing there: any finite codes (their weight is zero)
-#pragma unroll
-                    for (int k = 0; k < B; ++k) to[k] = 0;
-                }
-                load_page(phase + 2, i);
-            };
-            uint32_t lane_at[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) lane_at[k] = chunk_at(KT, ln.row, ln.group, k);
-            auto store = [&](auto bf16, int i, int u, uint32_t dst) {
-                uint32_t out[16];
-                widen32<B, decltype(bf16)::value>(raw[decltype(bf16)::value ? 0 : 1][i], out);
-                // (row & 7, which the swizzle goes by, is the lane's own where a unit
-                // has a multiple of eight rows, and flips bit 2 in odd units of four)
-                const uint32_t to = dst + u * Lane<D>::kRows * 128;
-                const uint32_t flip = Lane<D>::kRows % 8 == 0 ? 0u : (uint32_t)(u & 1) << 6;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sts128(to + (lane_at[k] ^ flip),
-                           make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]));
-            };
-            const float xscale = a.scale * 1.4426950408889634f;
-            // scales of a tile: four positions a lane, by the last widening warp, which
-            // looks up their page a tile before
-            float4 sk, sv;
-            bool sc_there = false;
-            int sc_page = -2;
-            auto load_scales_page = [&](int j) {
-                const int key = sp.begin + j * KT + 4 * lane;
-                if (4 * lane < KT && key < sp.end) {
-                    sc_page = kv_page(kb, c.num_pages, b, (int)pl.div_page(key));
-                } else {
-                    sc_page = -2;  // no position; -1: no such page
-                }
-            };
-            auto load_scales = [&](int j) {
-                const int key = sp.begin + j * KT + 4 * lane;
-                sc_there = sc_page >= 0;
-                if (sc_page == -1) report_status(status, HBL_ERR_INVALID_ARG);
-                if (sc_there) {
-                    const int64_t row = ((int64_t)sc_page * c.heads + h) * c.page_size +
-                                        (key - (int)pl.div_page(key) * c.page_size);
-                    sk = *reinterpret_cast<const float4*>(c.ks + row);
-                    sv = *reinterpret_cast<const float4*>(c.vs + row);
-                }
-                load_scales_page(j + 1);
-            };
-            auto store_scales = [&](int j) {
-                if (4 * lane >= KT) return;
-                const uint32_t sc = sc_s + (j % kScaleStages) * T::kScale;
-                const int key = sp.begin + j * KT + 4 * lane;
-                const float k4[4] = {sk.x, sk.y, sk.z, sk.w}, v4[4] = {sv.x, sv.y, sv.z, sv.w};
-                float ck[4], lv[4], rs[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // a position that is not there: 0 * x - inf
-                    const bool there = sc_there && key + e < sp.end;
-                    ck[e] = there ? __fmul_rn(k4[e], xscale) : 0.f;
-                    // a zero scale (an all-zero row: its codes are zero too) as 2^-100
-                    lv[e] = there ? fmaxf(lg2(v4[e]), -100.f) : -CUDART_INF_F;
-                    rs[e] = there ? ex2(-lv[e]) : 0.f;
-                }
-                auto f = [](float v) { return __float_as_uint(v); };
-                sts128(sc + lane * 32, make_uint4(f(ck[0]), f(ck[1]), f(lv[0]), f(lv[1])));
-                sts128(sc + lane * 32 + 16, make_uint4(f(ck[2]), f(ck[3]), f(lv[2]), f(lv[3])));
-                sts128(sc + KT * 8 + lane * 16, make_uint4(f(rs[0]), f(rs[1]), f(rs[2]), f(rs[3])));
-            };
-            const bool scales = cw == kConv - 1;
-            if (scales) {
-                load_scales_page(0);
-                load_scales(0);
-            }
-#pragma unroll
-            for (int i = 0; i < T::kMine; ++i) {
-                load_page(0, i);
-                load_page(1, i);
-            }
-#pragma unroll
-            for (int i = 0; i < T::kMine; ++i) load(0, i);
-#pragma unroll
-            for (int i = 0; i < T::kMine; ++i) load(1, i);
-            bool ok = true;
-#pragma unroll 1
-            for (int j = 0; j < tiles && ok; ++j) {
-                const int st = j & 1;
-                const uint32_t par = ((j >> 1) & 1) ^ 1;
-                if (scales) {
-                    if (j >= kScaleStages)
-                        ok = wait.all(scempty(j % kScaleStages), ((j / kScaleStages) & 1) ^ 1);
-                    if (!ok) break;
-                    store_scales(j);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(scfull(j % kScaleStages));
-                    load_scales(j + 1);
-                }
-                if (j >= 2) ok = wait.all(kempty(st), par);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < T::kMine; ++i) {
-                    const int u = unit(false, i);
-                    if (u < T::kUnits) store(ic_bool<true>{}, i, u, k_s + st * T::kStage);
-                    load(2 * j + 2, i);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_one(kfull(st));
-                if (j >= 2) ok = wait.all(vempty(st), par);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < T::kMine; ++i) {
-                    const int u = unit(true, i);
-                    if (u < T::kUnits) store(ic_bool<false>{}, i, u, v_s + st * T::kStage);
-                    load(2 * j + 3, i);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_one(vfull(st));
+            if (first.tiles > 0) widen(ic_bool<false>{}, first);
+            if (again()) {
+                widen(ic_bool<true>{}, task_of<D>(pl, c, kb, a, where, split));
+                done();
             }
         }
     }
     __syncwarp();
-    tmem_fence_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
-        tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
                      : "memory");
     }

@@ -398,10 +398,14 @@ HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_bat
  * [rows x num_heads] or NULL.  num_heads a multiple of num_kv_heads, at most
  * 65535; rows * num_heads <= 2^31 - 4096.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
  * past it are left out and reported); max_kv: about the longest sequence (0:
- * unknown), a hint that only speed depends on.  Codes and queries enter the
- * products exactly (few rows: queries below 2^-31 of their row's largest value
- * to within 2^-39 of it), sums and softmax are fp32; the probabilities that weight
- * V are rounded to fp16. */
+ * unknown), a hint that only speed depends on.
+ * V's scales: any finite ones from 0 on (a zero one stands with zero codes, 2^(bits-1), as
+ * the write leaves them; others count as 2^-60 of themselves there).  Where a sequence has
+ * one outside 2^-40 .. 2^40, its attention takes some three times the time.  Codes and
+ * queries enter the products exactly (few rows: queries below 2^-31 of their row's largest
+ * value to within 2^-39 of it), sums and softmax are fp32.  The weights of V's codes, each
+ * a probability times V's scale, are rounded to fp16, to 2^-12 of themselves; what is
+ * below 2^-31 of the row's largest such weight is left out of O (not of lse). */
 typedef struct {
     const uint16_t* Q;
     int64_t q_row_stride, q_head_stride;

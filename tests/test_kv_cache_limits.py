@@ -135,3 +135,146 @@ def test_tiny_rows_quantise_as_defined(D, bits, eps):
     page = int(c.table[0, 0])
     for pool, want in zip(pools(c.cache), (codes, scales, codes[::-1], scales[::-1])):
         assert same_bytes(pool[page, 0, :8], torch.from_numpy(want.copy()))
+
+# --------------------------------------------------------- V's scales, all of fp32
+
+def expected(c, causal=True, window=0):
+    """(O, lse, tolerance of each), fp64, for scales of any size.
+
+    As kv_reference.attention, with what wide scales add.  Exponents in log2 reach
+    |s| + |log2 sv| < 256, where fp32's half step is 2^-17: three roundings of the
+    exponent, the logarithm of the scale to 2^-22 of itself (150 * 2^-22), and the
+    difference of two reference points (2^-16): together below 2^-14 in nats.  A weight
+    p_i sv_i is held to 2^-12 of itself (here 2^-11), or to 2^-31 of the row's
+    largest one: 2^-30 of that times |code|.  A bf16's least half step is 2^-134."""
+    u = 2.0 ** -24
+    O = torch.zeros(c.rows, c.heads, c.D, dtype=torch.float64, device=DEV)
+    z = torch.full((c.rows, c.heads), -math.inf, dtype=torch.float64, device=DEV)
+    tol_O, tol_z = torch.zeros_like(O), torch.zeros_like(z)
+    group, r0 = c.heads // c.cache.num_kv_heads, 0
+    for b, (n, m) in enumerate(zip(c.new, c.lens)):
+        pos, key = torch.arange(m - n, m, device=DEV)[:, None], torch.arange(m, device=DEV)[None]
+        hidden = (key > pos) if causal else torch.zeros(n, m, dtype=torch.bool, device=DEV)
+        if window:
+            hidden = hidden | (key <= pos - window)
+        at = c.table[b].long()[key[0] // c.page], key[0] % c.page
+        for j in range(c.heads if n else 0):
+            h = j // group
+            k = c.stored(b, h, "k")
+            code = ref.unpack(c.cache.v_codes[at[0], h, at[1]], c.D, c.bits).double() - (
+                1 << (c.bits - 1))
+            sv = c.cache.v_scales[at[0], h, at[1]].double()
+            q = c.q[r0:r0 + n, j].double() * c.D ** -0.5
+            s = (q @ k.T).masked_fill(hidden, -math.inf)
+            lse = torch.logsumexp(s, 1)
+            p = torch.exp(s - lse[:, None].nan_to_num(neginf=0.0)) * sv
+            e = (4 * c.D + 2) * u * (q.abs() @ k.abs().T).masked_fill(hidden, 0).amax(1) + 2.0 ** -14
+            rows = slice(r0, r0 + n)
+            O[rows, j], z[rows, j] = p @ code, lse
+            tol_O[rows, j] = 2.0 ** -8 * O[rows, j].abs() + 2.0 ** -134 + \
+                (2 * e + 2.0 ** -11 + 4 * m * u)[:, None] * (p @ code.abs()) + \
+                2.0 ** -30 * p.amax(1, keepdim=True) * ((~hidden).double() @ code.abs())
+            tol_z[rows, j] = e + 2.0 ** -23 * lse.abs().nan_to_num(posinf=0.0) + m * u
+        r0 += n
+    return O, z, tol_O, tol_z
+
+
+def check(c, **kw):
+    O, lse = hbl.kv_attention(c.q, c.cache, *c.batch, max_rows=max(c.new), want_lse=True, **kw)
+    want, z, tol_O, tol_z = expected(c, **kw)
+    assert torch.isfinite(O.float()).all()
+    d = (O.double() - want).abs() - tol_O
+    assert float(d.max()) <= 0, (float(O.flatten()[d.argmax()]), float(want.flatten()[d.argmax()]))
+    none = z == -math.inf
+    assert torch.equal(lse == -math.inf, none)
+    d = (lse.double() - z).abs().masked_fill(none, 0) - tol_z
+    assert float(d.max()) <= 0, (float(lse.flatten()[d.argmax()]), float(z.flatten()[d.argmax()]))
+
+
+def scales_of(kind, shape, g):
+    """V scales [.., positions] of one kind (exponents; zero where nan)."""
+    e = torch.rand(shape, generator=g) - 0.5
+    pos = torch.arange(shape[-1]).expand(shape)
+    if kind == "tiny":
+        e = e - 110
+    elif kind == "subnormal":
+        e = 6 * e - 140
+    elif kind == "huge":
+        e = e + 125
+    elif kind == "spread":
+        e = 240 * e
+    elif kind == "zero_rows":       # beside rows of 2^34
+        e = torch.where(pos % 7 == 3, math.nan, e + 34)
+    elif kind == "zeros":
+        e = torch.full(shape, math.nan)
+    elif kind == "zeros_among":     # small ones and large ones that need no form of their own
+        e = torch.where(pos % 5 == 1, math.nan, 78 * e)
+    elif kind == "late":            # ordinary ones, then a few wild ones
+        e = torch.where(pos > shape[-1] - 9, 200 * e, e)
+    elif kind == "early":
+        e = torch.where(pos < 9, 200 * e, e)
+    elif kind == "edges":           # at and around where the kernels change their form
+        e = torch.where(pos % 2 == 0, -40.0, 40.0) + 0.02 * e
+    return torch.exp2(e.double()).float().nan_to_num(nan=0.0)
+
+
+KINDS = ["tiny", "subnormal", "huge", "spread", "zero_rows", "zeros", "zeros_among", "late", "early", "edges"]
+
+
+def wide_case(kind, new, lens, D, bits, qscale=2.0, **kw):
+    c = ref.Case(new, lens, D=D, bits=bits, page=16, seed=D + bits, qscale=qscale, **kw)
+    g = torch.Generator().manual_seed(D * bits)
+    for b, m in enumerate(lens):
+        pos = torch.arange(m)
+        sv = scales_of(kind, (c.cache.num_kv_heads, m), g).to(DEV)
+        page = c.table[b].long()[pos.to(DEV) // 16]
+        c.cache.v_scales[page, :, pos.to(DEV) % 16] = sv.T.contiguous()
+        # zero rows as the write leaves them: zero scales, zero values
+        zero = torch.from_numpy(oracle.kv_quant(np.zeros((1, D), np.uint16), bits)[0][0].copy())
+        for i in (sv[0] == 0).nonzero().flatten().tolist():
+            c.cache.v_codes[page[i], :, i % 16] = zero.to(DEV)
+    return c
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,bits", [(32, 8), (64, 3), (128, 4), (256, 2)])
+@pytest.mark.parametrize("new,lens", [([1, 3], [200, 777]), ([5, 1], [1500, 90]), ([40, 130], [300, 333])])
+def test_attention_of_any_value_scale(kind, D, bits, new, lens):
+    if kind == "huge" and bits > 2:     # (their values would pass fp32)
+        bits = 2
+    c = wide_case(kind, new, lens, D, bits, heads=4, kv_heads=2)
+    check(c)
+    # equal scores, where every row's share of the sum counts
+    c.q.zero_()
+    check(c)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["spread", "late", "zero_rows"])
+@pytest.mark.parametrize("causal,window", [(True, 100), (False, 0), (False, 50)])
+@pytest.mark.parametrize("new", [[2, 1], [70, 200]])
+def test_attention_of_any_value_scale_under_masks(kind, causal, window, new):
+    c = wide_case(kind, new, [260, 400], 64, 4, heads=4, kv_heads=2, qscale=0.5)
+    check(c, causal=causal, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("new", [[1, 2], [150, 40]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_that_make_up_for_the_scales(D, new):
+    # position i's score is -log of its V scale, between 2^-60 and 2^60: every term of O
+    # counts alike, and the normaliser is that of the rows of the smallest scales
+    c = wide_case("spread", new, [500, 3000], D, 4, heads=2, kv_heads=2)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    for b, m in enumerate(c.lens):
+        pos = torch.arange(m, device=DEV)
+        page, slot = c.table[b].long()[pos // 16], pos % 16
+        e = (120 * torch.rand(2, m, generator=torch.Generator().manual_seed(b)) - 60).to(DEV)
+        c.cache.v_scales[page, :, slot] = torch.exp2(e).T.contiguous()
+        c.cache.k_scales[page, :, slot] = (e.abs() * math.log(2) * D ** 0.5).T.contiguous()
+        codes = torch.full((m, 2, D // 2), 0x88, dtype=torch.uint8, device=DEV)
+        codes[:, :, 0] = torch.where(e.T > 0, 0x87, 0x89).to(torch.uint8)  # the first value -1 or 1
+        c.cache.k_codes[page, :, slot] = codes
+    check(c)
