@@ -526,6 +526,38 @@ def _kv_rows(t, cache, name, heads=None):
     return sr if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
 
 
+def _kv_overlap(rows, heads, D, a, b=None):
+    """Whether two strided [rows, heads, D] tensors share an element, each given as (first
+    element, row stride, head stride), strides not negative; without b, whether
+    elements of a are elements of a twice."""
+    if rows == 0 or heads == 0:
+        return False
+    if b is None:
+        # one dimension's steps hold the other's whole extent
+        for (n, s), (m, t) in (((heads, a[2]), (rows, a[1])), ((rows, a[1]), (heads, a[2]))):
+            if (n == 1 or s >= D) and (m == 1 or t >= (n - 1) * (s if n > 1 else 0) + D):
+                return False
+    else:
+        ends = [at + (rows - 1) * r + (heads - 1) * h + D for at, r, h in (a, b)]
+        if ends[0] <= b[0] or ends[1] <= a[0]:
+            return False
+        if a[1] == b[1] and a[1] > 0:  # side by side in rows of one stride
+            width, off = (heads - 1) * a[2] + D, (b[0] - a[0]) % a[1]
+            if width <= off and off + (heads - 1) * b[2] + D <= a[1]:
+                return False
+    import torch
+
+    # all pieces of D elements in order: two neighbours that overlap, of either tensor
+    starts = [(at + torch.arange(rows)[:, None] * r + torch.arange(heads) * h).flatten()
+              for at, r, h in ((a,) if b is None else (a, b))]
+    if b is None:
+        order = starts[0].sort().values
+        return bool((order[1:] - order[:-1] < D).any())
+    first = starts[0].sort().values
+    next_ = torch.searchsorted(first, starts[1] - D, right=True)  # the first that ends behind
+    return bool((first[next_.clamp(max=len(first) - 1)] - starts[1]).abs().lt(D).any())
+
+
 def _kv_call(what, cache, *args):
     """Calls the library on the cache's device and that device's current stream."""
     k, ks, v, vs = cache._tensors
@@ -591,6 +623,8 @@ def kv_cache_read(cache, cu_seqlens, kv_lens, block_table, rows, dtype=None, out
             _dev(t, dtype, "out")
             if tuple(t.shape) != shape or t.device != cache._device:
                 raise ValueError("out must be two [rows, heads, D] tensors on the cache's device")
+        if abs(K.data_ptr() - V.data_ptr()) < K.numel() * K.element_size():
+            raise ValueError("out must be two tensors that do not overlap")
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
     _kv_call("hbl_kv_cache_read", cache, cache._args, batch, K.data_ptr(), V.data_ptr(),
              1 if dtype == _torch.float32 else 0, _kv_status(status, cache))
@@ -623,21 +657,32 @@ def kv_attention(Q, cache, cu_seqlens, kv_lens, block_table, max_rows=None, max_
     1/sqrt(D); window 0 is none.  max_rows (no sequence has more rows) and max_kv
     (about the longest sequence) are host-side sizes that the launch is planned
     with; without them the row count and the block table's width are taken.
-    Returns O (out if given), with want_lse also lse fp32 [rows, q heads]."""
+    out may be Q itself, but must not overlap it otherwise.  Returns O (out if given), with want_lse also lse fp32 [rows, q heads]."""
     q_row, q_head = _kv_rows(Q, cache, "Q")
     rows, heads, D = Q.shape
+    q_ptr = Q.data_ptr()
     if out is None:
         out = _torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty((rows, heads, D))
         o_row, o_head = heads * D, D
+        o_ptr = out.data_ptr()
     else:
         o_row, o_head = _kv_rows(out, cache, "out", heads)
         if out.shape[0] != rows:
             raise ValueError("out must have Q's shape")
-        if (rows > 1 and o_row == 0) or (heads > 1 and o_head == 0):
-            raise ValueError("out must not be expanded: its rows and heads would overlap")
+        # rows of heads that hold D values each, apart from Q, need no closer look
+        o_ptr, width, down = out.data_ptr(), (heads - 1) * o_head + D, rows - 1
+        if (o_head < D and heads > 1 or o_row < width and down) and \
+                _kv_overlap(rows, heads, D, (0, o_row, o_head)):
+            raise ValueError("out's rows and heads must not overlap one another")
+        if q_ptr < o_ptr + 2 * (down * o_row + width) and \
+                o_ptr < q_ptr + 2 * (down * q_row + (heads - 1) * q_head + D):
+            # (Q itself will do: a row is read before it is written, by the same CTA)
+            q, o = (q_ptr >> 1, q_row, q_head), (o_ptr >> 1, o_row, o_head)
+            if q != o and _kv_overlap(rows, heads, D, q, o):
+                raise ValueError("out must not overlap Q, unless it is Q")
     lse = cache._tensors[1].new_empty((rows, heads)) if want_lse else None
     batch = _kv_batch(cache, cu_seqlens, kv_lens, block_table, rows)
-    args = _pack_attn(Q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,
+    args = _pack_attn(q_ptr, q_row, q_head, o_ptr, o_row, o_head,
                       lse.data_ptr() if want_lse else 0, heads, max_rows or 0, max_kv or 0,
                       D ** -0.5 if scale is None else scale, 1 if causal else 0, window)
     if ws is None:

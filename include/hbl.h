@@ -394,11 +394,12 @@ HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_bat
  * with i visible if i < kv_len, (causal) i <= p and (window w > 0) i > p - w.
  * A row that sees nothing has O = 0 and lse = -inf.  Stored bytes past a
  * sequence's length are never used, whatever they hold.
- * Q, O: bf16, strided as K above (O must not overlap Q); lse: fp32
- * [rows x num_heads] or NULL.  num_heads a multiple of num_kv_heads, at most
- * 65535; rows * num_heads <= 2^31 - 4096.  max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows
- * past it are left out and reported); max_kv: about the longest sequence (0:
- * unknown), a hint that only speed depends on.
+ * Q, O: bf16, strided as K above.  O's rows and heads must not overlap one another, nor
+ * Q, unless O is Q itself with its strides.  lse: fp32 [rows x num_heads] or NULL.
+ * num_heads a multiple of num_kv_heads, at most 65535; rows * num_heads <= 2^31 - 4096.
+ * max_rows: no sequence has more rows (0: unknown, `rows` is taken; rows past it are left
+ * out and reported); max_kv: about the longest sequence (0: unknown), a hint that only
+ * speed depends on.
  * V's scales: any finite ones from 0 on (a zero one stands with zero codes, 2^(bits-1), as
  * the write leaves them; others count as 2^-60 of themselves there).  Where a sequence has
  * one outside 2^-40 .. 2^40, its attention takes some three times the time.  Codes and

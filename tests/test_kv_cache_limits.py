@@ -278,3 +278,60 @@ def test_scores_that_make_up_for_the_scales(D, new):
         codes[:, :, 0] = torch.where(e.T > 0, 0x87, 0x89).to(torch.uint8)  # the first value -1 or 1
         c.cache.k_codes[page, :, slot] = codes
     check(c)
+
+# ------------------------------------------------------------ buffers that overlap
+
+def test_overlap_of_strided_rows():
+    # against all elements of both, over small layouts
+    g = np.random.default_rng(0)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        rows, heads, D = (int(g.integers(1, 5)) for _ in range(3))
+        a = (int(g.integers(0, 40)), int(g.integers(0, 12)), int(g.integers(0, 12)))
+        b = a if g.random() < 0.1 else tuple(int(v) for v in (g.integers(0, 40), g.integers(0, 12),
+                                                              g.integers(0, 12)))
+        if g.random() < 0.5:
+            b = (b[0], a[1], b[2])
+        cells = [{at + i * r + j * h + d for i in range(rows) for j in range(heads) for d in range(D)}
+                 for at, r, h in (a, b)]
+        want = bool(cells[0] & cells[1])
+        assert hbl._kv_overlap(rows, heads, D, a, b) == want, (rows, heads, D, a, b)
+        alone = len(cells[0]) < rows * heads * D
+        assert hbl._kv_overlap(rows, heads, D, a) == alone, (rows, heads, D, a)
+        seen[want] += 1
+    assert min(seen.values()) > 500
+
+
+@gpu
+@pytest.mark.parametrize("rows", [2, 150])
+def test_attention_outputs_that_overlap(rows):
+    c = ref.Case([rows], [rows + 300], heads=4, kv_heads=2, D=64, bits=4, seed=rows)
+    want = hbl.kv_attention(c.q, c.cache, *c.batch)
+    wide = torch.zeros(rows + 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    wide[:-1] = c.q
+    for out in (wide[1:], wide.view(-1)[8:8 + c.q.numel()].view(rows, 4, 64)):
+        with pytest.raises(ValueError):
+            hbl.kv_attention(wide[:-1], c.cache, *c.batch, out=out)
+    # rows or heads of the output over one another
+    flat = torch.zeros(4 * rows * 256, dtype=torch.bfloat16, device=DEV)
+    for strides in ((128, 64, 1), (256, 56, 1), (64, 64, 1)):
+        with pytest.raises(ValueError):
+            hbl.kv_attention(c.q, c.cache, *c.batch, out=flat.as_strided((rows, 4, 64), strides))
+    # side by side in one buffer, in either order of strides, and the queries themselves
+    fused = torch.zeros(rows, 8, 64, dtype=torch.bfloat16, device=DEV)
+    fused[:, :4] = c.q
+    assert torch.equal(hbl.kv_attention(fused[:, :4], c.cache, *c.batch, out=fused[:, 4:]), want)
+    assert torch.equal(fused[:, :4], c.q)
+    out = flat.as_strided((rows, 4, 64), (64, 64 * rows, 1))
+    assert torch.equal(hbl.kv_attention(c.q, c.cache, *c.batch, out=out), want)
+    q = c.q.clone()
+    assert torch.equal(hbl.kv_attention(q, c.cache, *c.batch, out=q), want)
+
+
+@gpu
+def test_read_outputs_that_overlap():
+    c = ref.Case([6], [20], heads=2, kv_heads=2, D=64, bits=4)
+    x = torch.zeros(9, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for out in ((x[:6], x[:6]), (x[:6], x[3:])):
+        with pytest.raises(ValueError):
+            hbl.kv_cache_read(c.cache, *c.batch, 6, out=out)
