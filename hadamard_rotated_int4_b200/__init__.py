@@ -49,7 +49,7 @@ EXPORTS = ("hbl_status_string", "hbl_version", "hbl_workspace_size", "hbl_worksp
            "hbl_kv_cache_write", "hbl_kv_cache_read", "hbl_kv_attention_workspace",
            "hbl_kv_attention",
            "hbl_expand_ternary", "hbl_ternary_gemm_s8w", "hbl_selftest_bounded_wait",
-           "hbl_probe_tc_int8")
+           "hbl_selftest_clock_wait", "hbl_probe_tc_int8")
 
 _lib = None
 _kv_calls = {}  # the KV calls once more, taking packed bytes for their structs
@@ -149,6 +149,8 @@ def lib():
         L.hbl_ternary_gemm_s8w.argtypes = [P, P, I, I, I, P, P, I, P, P, P, P]
         L.hbl_selftest_bounded_wait.restype = I
         L.hbl_selftest_bounded_wait.argtypes = [I, I, P, P]
+        L.hbl_selftest_clock_wait.restype = I
+        L.hbl_selftest_clock_wait.argtypes = [I, I, I, P, P]
         L.hbl_probe_tc_int8.restype = I
         L.hbl_probe_tc_int8.argtypes = [I, I, P, P]
         _lib = L
@@ -733,6 +735,12 @@ def selftest_bounded_wait(arrive, timeout_us, status):
     """hbl_selftest_bounded_wait: the bounded-wait failure path on one probe kernel."""
     _check(lib().hbl_selftest_bounded_wait(int(bool(arrive)), int(timeout_us), _ptr(status),
                                            _stream()), "hbl_selftest_bounded_wait")
+
+
+def selftest_clock_wait(arrive, aborted, limit_clocks, status):
+    """hbl_selftest_clock_wait: the attention kernels' wait on one probe kernel."""
+    _check(lib().hbl_selftest_clock_wait(int(bool(arrive)), int(bool(aborted)), int(limit_clocks),
+                                         _ptr(status), _stream()), "hbl_selftest_clock_wait")
 
 
 def probe_tc_int8(ctas, mmas_per_cta, status):

@@ -908,6 +908,18 @@ hbl_status hbl_selftest_bounded_wait(int arrive, int timeout_us, int32_t* dev_st
                                      static_cast<cudaStream_t>(stream));
 }
 
+hbl_status hbl_selftest_clock_wait(int arrive, int aborted, int limit_clocks, int32_t* dev_status,
+                                   void* stream) {
+    if (dev_status == nullptr) return HBL_ERR_INVALID_ARG;
+    if (limit_clocks < 1 || limit_clocks > 2000000000) return HBL_ERR_INVALID_ARG;
+    if (!aligned16(dev_status)) return HBL_ERR_ALIGNMENT;
+    int sms = 0;
+    hbl_status st = device(&sms);
+    if (st != HBL_OK) return st;
+    return launch_clock_wait_probe(arrive, aborted, limit_clocks, dev_status,
+                                   static_cast<cudaStream_t>(stream));
+}
+
 hbl_status hbl_probe_tc_int8(int ctas, int mmas_per_cta, int32_t* dev_status, void* stream) {
     if (dev_status == nullptr) return HBL_ERR_INVALID_ARG;
     if (ctas < 1 || ctas > 4096 || mmas_per_cta < 1 || mmas_per_cta > (1 << 22))

@@ -161,15 +161,20 @@ __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void or_shared(uint32_t at, uint32_t v) {
+    asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 // ------------------------------------------------------------ waits of a pipeline
 
-// Waits for an mbarrier phase, for at most about two seconds (in SM clocks), and
+// Waits for an mbarrier phase, for at most `limit` SM clocks (about two seconds), and
 // while *abort_flag (if given) is zero.  Polls in a bare loop and looks at the flag
 // and the clock now and then only: in kernels that hand over every few hundred
 // cycles, reading the global timer at each failed poll costs more than the wait.
+constexpr int64_t kWaitClocks = 4000000000ll;
 __device__ __forceinline__ bool mbar_wait_clock(uint32_t bar, uint32_t parity,
-                                                const volatile int* abort_flag) {
-    constexpr int64_t kLimit = 4000000000ll;
+                                                const volatile int* abort_flag,
+                                                int64_t limit = kWaitClocks) {
     int64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
         if (mbar_test_parity(bar, parity)) return true;
@@ -177,7 +182,7 @@ __device__ __forceinline__ bool mbar_wait_clock(uint32_t bar, uint32_t parity,
             if (abort_flag != nullptr && *abort_flag) return false;
             const int64_t t = clock64();
             if (t0 == 0) t0 = t;
-            if (t - t0 > kLimit) return false;
+            if (t - t0 > limit) return false;
         }
     }
 }

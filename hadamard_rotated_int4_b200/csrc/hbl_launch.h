@@ -137,6 +137,8 @@ hbl_status launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttn&
 // Self-test of the bounded-wait failure path (see k9_selftest.cu).
 hbl_status launch_bounded_wait_probe(int arrive, int timeout_us, int32_t* status,
                                      cudaStream_t stream);
+hbl_status launch_clock_wait_probe(int arrive, int aborted, int limit_clocks, int32_t* status,
+                                   cudaStream_t stream);
 
 // Dense INT8 tensor-core rate probe (see k9_tc_probe.cu).
 hbl_status launch_tc_int8_probe(int ctas, int mmas_per_cta, int32_t* status, cudaStream_t stream);

@@ -146,9 +146,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
     const uint32_t ring = smem_addr(smem) + warp * St::kCount * St::kBytes;
     const uint32_t bars = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + warp * 32;
     if (lane < St::kCount) mbar_init_count(bars + 8 * lane, 1);
-    // a flag behind the first warp's barriers (at most three): V's scales need a second pass
-    const uint32_t odd_s = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + 24;
-    if (threadIdx.x == 0) sts32(odd_s, 0);
+    // flags behind the first warp's barriers (at most three): 1, V's scales need a second pass;
+    // 2, a wait gave up
+    const uint32_t flags_s = smem_addr(smem) + smem_bytes<D, B, NT>() - kWarps * 32 + 24;
+    if (threadIdx.x == 0) sts32(flags_s, 0);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
     int done = 0;  // stages of this warp's ring that have been used
@@ -522,18 +523,20 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                 issue(it + St::kCount, next_page);
                 next_page = page_of(it + St::kCount + 1);
             }
-            // after a timeout: the copies still in flight, before their stages are reused
-            for (int j = it + 1; j < steps && j < it + St::kCount; ++j)
+            // after a timeout: the copies still in flight, the late one among them
+            for (int j = it; j < steps && j < it + St::kCount; ++j)
                 mbar_wait_clock(bars + 8 * ((done + j) % St::kCount), ((done + j) / St::kCount) & 1,
                                 nullptr);
             done += steps;
             return it < steps;
         };
-        bool late = pass(ic_bool<false>{});
-        if (odd) sts32(odd_s, 1);
+        if (pass(ic_bool<false>{})) or_shared(flags_s, 2);
+        if (odd) or_shared(flags_s, 1);
         __syncthreads();  // (the rings are free as well)
-        bool apart = __builtin_expect(lds32(odd_s) != 0, 0);
+        const uint32_t raised = lds32(flags_s);
+        bool apart = __builtin_expect(raised != 0, 0);
         if (apart) {  // unless they were zero scales alone
+            if (raised & 2u) return;  // nothing is stored of a part that lacks positions
             bool far = false;
             for (int key = begin + threadIdx.x; key < end; key += kThreads) {
                 const int pi = (int)pl.div_page(key), page = kv_page(kb, c.num_pages, b, pi);
@@ -542,13 +545,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                                             (key - pi * c.page_size)]);
             }
             apart = __syncthreads_or(far);
-            if (threadIdx.x == 0) sts32(odd_s, 0);
+            if (threadIdx.x == 0) sts32(flags_s, 0);
         }
         if (__builtin_expect(apart, 0)) {
-            if (!late) {
-                start();
-                late = pass(ic_bool<true>{});
-            }
+            start();
+            const bool late = pass(ic_bool<true>{});
             // both sums against the point half way between theirs
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                         O[k][n][2 + e] *= up;
                     }
                 }
-            __syncthreads();
+            if (__syncthreads_or(late)) return;
         }
         // ---- join the warps.  Lane (g, t): values NV g .. of rows 2t, 2t + 1
 #pragma unroll
@@ -622,9 +623,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                 if (d == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M - kShift, L);
             }
         }
-        // the rings' memory goes back to the copies; a CTA that has lost one ends here
+        // the rings' memory goes back to the copies
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (__syncthreads_or(late) || at >= stop) return;
+        __syncthreads();
+        if (at >= stop) return;
     }
 }
 

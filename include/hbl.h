@@ -29,7 +29,8 @@
  *     launched.  Errors are returned before any launch; nothing is written then.
  *   - `dev_status` (nullable) is a device int32 the kernels set to a non-zero
  *     hbl_status if a bounded device-side wait gives up (HBL_ERR_TIMEOUT); the
- *     caller reads it after synchronising.  Kernels never trap.
+ *     caller reads it after synchronising (the call's results are then undefined).
+ *     Kernels never trap.
  *   - Shapes: K is a power of two with 16 <= K <= 32768 (the fast transform
  *     needs a power of two); M >= 0 (M == 0 launches nothing); N >= 16 and
  *     N % 16 == 0.  Violations return HBL_ERR_SHAPE.
@@ -462,6 +463,12 @@ HBL_API hbl_status hbl_ternary_gemm_s8w(const void* codes, const float* scales, 
  * in [1, 1000000]. */
 HBL_API hbl_status hbl_selftest_bounded_wait(int arrive, int timeout_us, int32_t* dev_status,
                                              void* stream);
+
+/* The same of the attention kernels' wait, which counts SM clocks and also gives up when
+ * its abort flag is set (aborted != 0; the other warps of a CTA that lost a wait leave
+ * theirs by it).  limit_clocks in [1, 2000000000]. */
+HBL_API hbl_status hbl_selftest_clock_wait(int arrive, int aborted, int limit_clocks,
+                                           int32_t* dev_status, void* stream);
 
 /* Dense INT8 tensor-core rate probe (no counterpart on the pages; it measures
  * the denominator of the ternary GEMM's roofline on the GPU at hand).  Launches

@@ -335,3 +335,31 @@ def test_read_outputs_that_overlap():
     for out in ((x[:6], x[:6]), (x[:6], x[3:])):
         with pytest.raises(ValueError):
             hbl.kv_cache_read(c.cache, *c.batch, 6, out=out)
+
+# --------------------------------------------------------------------- lost waits
+
+def test_clock_wait_probe_is_checked_on_the_host():
+    call = hbl.lib().hbl_selftest_clock_wait
+    assert call(0, 0, 1000, None, None) == 1
+    assert call(0, 0, 0, 0x10000, None) == 1 and call(0, 0, 2000000001, 0x10000, None) == 1
+    assert call(0, 0, 1000, 0x10004, None) == 3
+
+
+@gpu
+@pytest.mark.parametrize("arrive,aborted,limit,want",
+                         [(1, 0, 1000, 0), (0, 0, 2000000, 7), (0, 1, 2000000000, 7), (1, 1, 1000, 0)])
+def test_the_attention_s_wait_gives_up_by_time_and_by_its_flag(arrive, aborted, limit, want):
+    status = hbl.new_status(DEV)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    hbl.selftest_clock_wait(1, 0, 1000, status)  # (loaded)
+    begin.record()
+    hbl.selftest_clock_wait(arrive, aborted, limit, status)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status[0]) == want
+    # 2e6 clocks are some 1 to 2 ms; the flag does not wait for its second
+    ms = begin.elapsed_time(end)
+    assert ms < 100 and (want == 0 or aborted or ms > 0.5)
+    c = ref.Case([1, 40], [70, 90], heads=4, kv_heads=2, D=64, bits=4)  # the context is usable
+    O, lse = hbl.kv_attention(c.q, c.cache, *c.batch, want_lse=True)
+    ref.check_attention(c, O, lse)
