@@ -363,3 +363,26 @@ def test_the_attention_s_wait_gives_up_by_time_and_by_its_flag(arrive, aborted, 
     c = ref.Case([1, 40], [70, 90], heads=4, kv_heads=2, D=64, bits=4)  # the context is usable
     O, lse = hbl.kv_attention(c.q, c.cache, *c.batch, want_lse=True)
     ref.check_attention(c, O, lse)
+
+# ------------------------------------------------------------------- side by side
+
+@gpu
+@pytest.mark.parametrize("new,lens", [([1, 1], [5000, 300]), ([70], [4000]), ([40, 1, 130], [900, 3000, 1500])])
+def test_calls_on_several_streams_give_what_one_gives(new, lens):
+    # split pieces, split ranges and both kernels of a mixed batch, three streams at once,
+    # a workspace of the call's own each time
+    cases = [ref.Case(new, lens, heads=8, kv_heads=2, D=128, bits=4, seed=s) for s in range(3)]
+    call = lambda c: hbl.kv_attention(c.q, c.cache, *c.batch, max_rows=max(new), want_lse=True)
+    alone = [call(c) for c in cases]
+    assert hbl.kv_attention_workspace_size(sum(new), 8, cases[0].cache, len(new),
+                                           cases[0].table.shape[1], max_rows=max(new)) > 0
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                outs.append((i, call(c)))
+    torch.cuda.synchronize()
+    for i, (O, lse) in outs:
+        assert torch.equal(O, alone[i][0]) and torch.equal(lse, alone[i][1])
