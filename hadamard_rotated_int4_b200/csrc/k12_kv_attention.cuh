@@ -12,6 +12,35 @@
 #include "hbl_kv.cuh"
 
 namespace hbl {
+
+// ---- arithmetic of the kernels
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2_any(float x) {  // subnormal x too
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Two fp32 -> an fp16 pair (low half = first), round to nearest even.
+__device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 namespace k12 {
 
 // How a launch is laid out; made on the host from sizes alone (few_plan,
@@ -102,11 +131,6 @@ __device__ __forceinline__ bool folds(float sv) {  // zero, or of 2^-kFold .. 2^
     constexpr uint32_t kSpan = (uint32_t)(2 * (int)kFold) << 23;
     const uint32_t bits = __float_as_uint(sv);
     return bits == 0 || bits - kLow <= kSpan;
-}
-__device__ __forceinline__ float lg2_any(float x) {  // subnormal x too
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // Partial results of chunks: [split][packed row][query head] x (D values, m, sum, 2 unused).

@@ -102,26 +102,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-__device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 template <int D, int B, int NT>
 __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
@@ -442,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>)
                                 // (stored where nothing is, it may be anything: -inf stays -inf)
                                 const uint32_t sc = st + 2 * St::kCodes + St::kScales +
                                                     4 * (16 * (b0 + blk) + kslot + 8 * u);
-                                const float any = k12::lg2_any(__uint_as_float(lds32(sc)));
+                                const float any = lg2_any(__uint_as_float(lds32(sc)));
                                 const float lv = fminf(fmaxf(any, k12::kNoScale), 128.f);
                                 rsv[blk][u] = 0.f;
 #pragma unroll

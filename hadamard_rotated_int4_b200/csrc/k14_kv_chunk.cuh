@@ -145,26 +145,6 @@ template <int N>
 __device__ __forceinline__ void reg_dealloc() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // Bounded wait; on expiry (here or, through the flag, anywhere in the CTA) false.
 // one(): by a single thread.  all(): by a whole warp, whose lanes leave it
@@ -901,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
                 const bool there = sc_there && key + e < sp.end;
                 ck[e] = there ? __fmul_rn(k4[e], xscale) : 0.f;
                 if constexpr (APART) {
-                    lv[e] = there ? fmaxf(k12::lg2_any(v4[e]), k12::kNoScale) : kNowhere;
+                    lv[e] = there ? fmaxf(lg2_any(v4[e]), k12::kNoScale) : kNowhere;
                     rs[e] = 0.f;  // (not used)
                 } else {
                     lv[e] = there ? fmaxf(lg2(v4[e]), k12::kZeroFold) : -CUDART_INF_F;
