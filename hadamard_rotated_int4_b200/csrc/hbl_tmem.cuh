@@ -1,4 +1,5 @@
-// hbl_tmem.cuh -- tensor-memory loads and stores in the 16-lane shapes.
+// hbl_tmem.cuh -- tensor-memory loads and stores in the 16-lane shapes, and a load of
+// 32 lanes, a row a thread.
 //
 // 16x256b: thread (g = lane / 4, t = lane % 4) of a warp holds, of each group of
 // 8 columns k, r[4k], r[4k+1] = lane g, columns 8k + 2t, 8k + 2t + 1 and

@@ -12,10 +12,11 @@
 // Both kernels are bound by HBM at large batches, close behind by the instructions of
 // coding and placing a row (three quarters of all issue slots), and by launch
 // latency at one decoding step.  Measured, graph replay: 131071 rows of 8 heads of 128
-// out of the 4-bit cache as bf16 108.5 us, 0.96 of the measured copy bandwidth; 8192
-// tokens of 32 heads into the 3-bit cache 38 us, 0.65 of it; 64 tokens of 8 heads
-// 3.0 us to write and 3.3 us to read.  A warp takes one token and 1..kSteps steps of its 2 * heads
-// head rows (K heads, then V heads; D/16 lanes a row, 16 values a lane): the
+// out of the 4-bit cache as bf16 107 us, 0.97 of the measured copy bandwidth; 8192
+// tokens of 32 heads into the 3-bit cache 37.4 us, 0.66 of it; 64 tokens of 8 heads
+// 2.8 us to write and 3.2 us to read, 1024 tokens of as many sequences 11.4 and 11.0
+// (a token's search goes over 32 sequences at a time).  A warp takes one token and
+// 1..kSteps steps of its 2 * heads head rows (K heads, then V heads; D/16 lanes a row, 16 values a lane): the
 // token's sequence, position and page are found once per warp, by one round of
 // loads and a ballot per 32 sequences instead of a chain of dependent loads.
 #include "hbl_kv_codes.cuh"

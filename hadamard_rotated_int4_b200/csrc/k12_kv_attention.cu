@@ -115,14 +115,17 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // SMs that the plans count on (the workspace must not depend on the device).
 constexpr int kSizingSms = 148;
-// Row blocks that see at most this many positions are not split.  Not splitting saves
+// Row blocks that see at most this many positions, by the block table's width and the
+// window (a wider table counts as long, whatever the lengths in it), are not split.  Not splitting saves
 // a launch (22 -> 17 us a call, host included), and on the GPU, 8 cached heads of 128
 // at 4 bits, one sequence of 517: 9.5 against 11.4 us split, 8 of 1000: 11.5 / 14.0,
-// 256 of 400: 43 / 71; one of 1000 takes 11.0 / 8.5, 64 of 1000: 30.9 / 29.4.
+// 256 of 400: 43 / 71; one of 1000 takes 11.0 / 8.5, 64 of 1000: 30.9 / 29.4.  (With V's
+// scales looked over, the first is 10.1 now, under a table of 2048 pages 12.8.)
 constexpr int kWhole = 1024;
 // Sequences with at most this many head rows go to the few-rows kernel.  16 sequences
 // of 4000, 4 query heads to each of 8 cached ones: 32 head rows take 61 us there and
-// 87.5 us in chunks, 48 take 83.5 and 87.9, 64 take 101.5 and 88.3.
+// 87.5 us in chunks, 48 take 83.5 and 87.9, 64 take 101.5 and 88.3.  (Measured at D = 128
+// alone; other head sizes go by it.)
 constexpr int kFewRows = 32;
 
 // Round-up reciprocal of the page size: exact for x < 2^31.

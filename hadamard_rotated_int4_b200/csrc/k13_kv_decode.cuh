@@ -8,7 +8,7 @@
 // in one pass with the running m: taking V's scale into the exponent leaves the
 // integer codes as the second product's operand, and the weights 2^(x_i - m)
 // in (0, 2^8], so that fp16 holds them (times 2^6; what is below 2^-31 of
-// the reference is lost, a term's rounding is 2^-12 of itself).  Where 1 / sv or a weight
+// the reference is lost, a term's rounding is 2^-11 of itself).  Where 1 / sv or a weight
 // leaves fp32's range, which takes V scales outside 2^-40 .. 2^40, a part is worked on
 // once more with its normaliser summed apart (k12_kv_attention.cuh).
 //
@@ -35,9 +35,11 @@
 // passes it by more than 2^8.
 //
 // Measured, graph replay, D = 128, 32 query heads over 8: 64 sequences of 1024 to
-// 8192 on the 4-bit cache 76 us (44 to read it once), two of 131071 on the 3-bit one
-// 73 us (33); five rows of each of 16 sequences, 8-bit, 32 heads of 64, 68 us (44).
-// Loads alone take 60 and 43 us in the first two, all but the widening 63 and 54.
+// 8192 on the 4-bit cache 75 us (44 to read it once), two of 131071 on the 3-bit one
+// 75 us (33); five rows of each of 16 sequences, 8-bit, 32 heads of 64, 69 us (44).
+// Loads alone take 60 and 43 us in the first two, all but the widening 63 and 54.  With
+// a V scale outside 2^-40 .. 2^40 in every part the first takes 167 us, with zero rows
+// 95 (a look at all scales; both timed as calls, 83 without).
 // Tried and slower: four CTAs an SM with steps of 32 positions (84 against 76 us),
 // 16 or 32 positions at a time within a step (82, 78), copies that run ahead into the
 // next part (79: the other CTAs of the SM cover the gap already).

@@ -38,11 +38,16 @@
 // bounds it: 3300 cycles for 64 positions, where the products take 1300.
 //
 // Measured, graph replay: 4-bit, D = 128, a prompt of 8192 against itself with 32
-// query heads over 8: 713 us, 771 TFLOP/s, 0.47 of the measured bf16 rate; 5200 cycles
+// query heads over 8: 699 us, 786 TFLOP/s, 0.48 of the measured bf16 rate; 5100 cycles
 // for 128 positions and two row sets, of which the products with their hand-overs
 // alone (nothing widened, no exponentials) take 3700; some 12 us of every CTA are its
 // start (block, barriers, queries: 5) and end (last products, results: 3) and
 // the filling of its pipeline.
+//
+// Measured as well: heads of 64 634 us, of 32 572 us (the exponentials are as many);
+// 16 heads over 2 of 256 and 4096 positions 253 us.  The second pass that wide V scales
+// take: 2.4 ms instead of 0.7.  It works on 16 rows at a time: with all 32 of a warp at
+// once its registers cost the first pass 2 % (725 us).
 //
 // Tried and slower: 24 warps with a pair to each row quarter, half the columns each
 // (6380 cycles); weights computed against the reference of the part before while the

@@ -406,7 +406,7 @@ HBL_API hbl_status hbl_kv_cache_read(const hbl_kv_cache* cache, const hbl_kv_bat
  * one outside 2^-40 .. 2^40, its attention takes some three times the time.  Codes and
  * queries enter the products exactly (few rows: queries below 2^-31 of their row's largest
  * value to within 2^-39 of it), sums and softmax are fp32.  The weights of V's codes, each
- * a probability times V's scale, are rounded to fp16, to 2^-12 of themselves; what is
+ * a probability times V's scale, are rounded to fp16, to 2^-11 of themselves; what is
  * below 2^-31 of the row's largest such weight is left out of O (not of lse). */
 typedef struct {
     const uint16_t* Q;
