@@ -615,8 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(KvCache c, KvBatch k
         // has landed with the drain's single phase (a set's last product alone could not
         // be told from the one before the one before it by a parity).
         if (ok && parts > 0) ok = wait.all(bar.drain(), 0);
-        // (the flag stands since the last part's scales, which this warp has waited for)
-        if (ok && (APART || lds32(odd_s) == 0)) {
+        // (Both flags stand: a wait that another warp lost, which left products out, since
+        // before the drain; the scales' since the last part's, which this warp has waited for.)
+        if (ok && *abort_flag == 0 && (APART || lds32(odd_s) == 0)) {
             tmem_fence_after();
             // row 8k + g's sum and reference sit in lane 4g
             float L = 0.f, M = 0.f;
